@@ -242,6 +242,126 @@ flint_status_t flint_attn_decode(const flint_decode_params_t* params,
                                  void* out, float* lse,
                                  void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---- Paged KV cache ---------------------------------------------------------
+ * For serving: the keys and values of many sequences in pages of one pool, in
+ * place of flint_attn_decode's one dense cache per sequence (a KV cache appears
+ * on the Flint config page through use_cache; paging is this library's own).
+ * flint_attn_paged_append fills the cache (a prompt after flint_attn_fwd, a
+ * chunk of one, single tokens, any mix); flint_attn_decode_paged appends one new
+ * token per sequence and attends with it.
+ *
+ * Position t of sequence b lives in page block_table[b * table_stride + t / P],
+ * slot t % P (P = page_size). KV head g's 128 channels start at element
+ *   page * page_stride + g * head_stride + (t % P) * token_stride
+ * of k_pages (normalised, rotated keys) and of v_pages alike, so head-major
+ * [pages, Hk, P, D] and token-major [pages, P, Hk, D] pools, and K and V side by
+ * side in one tensor, are all taken. Sequences may share pages (a common
+ * prefix); a slot that a call writes must belong to one sequence alone.
+ *
+ * Cache types: bfloat16, or e4m3 (one byte, 4 exponent and 3 mantissa bits, no
+ * infinities), which holds x / scale[g] rounded to nearest even and saturated to
+ * +-448, with one float per KV head for K and one for V (null: 1).
+ *
+ * cache_lens[b] is the number of tokens that sequence b has cached. -1 marks a
+ * row that is not in use (a batch padded to a fixed size): nothing of it is read
+ * or written, its rows of out and lse included. Table entries past a sequence's
+ * last token, and those of pages that lie wholly before its window, are not read.
+ *
+ * Errors found on the device set the status word and nothing out of range is
+ * touched; flint_attn_check_status() then returns FLINT_ERR_INVALID_ARG:
+ *   - a cache_lens entry below -1 or past the table (slot cache_lens[b] must
+ *     exist, max_pages * P slots per sequence): the sequence is skipped, its out
+ *     and lse rows stay as they were (append: its tokens past the table are
+ *     skipped);
+ *   - a table entry outside [0, num_pages): append skips the token; decode writes
+ *     NaN to the out and lse rows of the KV heads' queries that needed the page.
+ * The status word is not cleared by a call; flint_attn_check_status clears it. */
+typedef enum { FLINT_CACHE_BF16 = 0, FLINT_CACHE_E4M3 = 1 } flint_cache_dtype_t;
+
+typedef struct {
+  int32_t num_pages;        /* pages in the pool, >= 1 */
+  int32_t page_size;        /* P: slots per page, a multiple of 16 */
+  int32_t max_pages;        /* columns of block_table, >= 1; max_pages * P < 2^31 */
+  int32_t num_kv_heads;     /* Hk */
+  int32_t head_dim;         /* D; must be 128 */
+  int32_t cache_dtype;      /* flint_cache_dtype_t */
+  int64_t page_stride;      /* elements; multiples of 16 bytes, >= 128. All three 0: */
+  int64_t head_stride;      /* contiguous [num_pages, Hk, P, D]                      */
+  int64_t token_stride;
+  int64_t table_stride;     /* elements between rows of block_table; 0: max_pages */
+} flint_paged_cache_t;
+
+typedef struct {
+  flint_paged_cache_t cache;
+  int32_t num_seqs;         /* N >= 1 sequences */
+  int32_t total_tokens;     /* T >= 0 rows of k and v */
+  int32_t use_rope;         /* NeoX RoPE at the token's position */
+  float rope_theta;
+  float rms_eps;
+  int32_t dtype;            /* FLINT_BF16 (k, v, k_norm_w) */
+  int64_t k_stride;         /* elements between tokens of k (rows [Hk, D] contiguous), */
+  int64_t v_stride;         /* multiples of 8; 0: Hk * D                               */
+} flint_paged_append_params_t;
+
+/* Appends rows cu_new_lens[b] .. cu_new_lens[b+1] of k and v (raw projections,
+ * [T, Hk, D] bfloat16) to sequence b, from position cache_lens[b] on: k_hat =
+ * RoPE(RMSNorm(k)) and v, rounded to the cache's type, into their slots. Rows at
+ * or past cu_new_lens[N] are not read (a fixed-size buffer partly filled).
+ *   cu_new_lens [N+1] int32 (device, non-decreasing from 0; its last entry may be
+ *   below T but not above it), cache_lens [N] int32 (device; not advanced),
+ *   status: caller-owned device int32[64], 256-byte aligned, status[0] = 0 before
+ *   its first use (the layout flint_attn_check_status takes).
+ * With T = 0 k and v may be null and nothing is launched. */
+flint_status_t flint_attn_paged_append(const flint_paged_append_params_t* params,
+                                       const void* k, const void* v, const void* k_norm_w,
+                                       const int32_t* cu_new_lens, const int32_t* cache_lens,
+                                       const int32_t* block_table, void* k_pages, void* v_pages,
+                                       const float* k_scale, const float* v_scale,
+                                       int32_t* status, void* stream);
+
+typedef struct {
+  flint_paged_cache_t cache;
+  int32_t batch;            /* B >= 1 rows, one new token each */
+  int32_t num_q_heads;      /* H; H % Hk == 0, H / Hk <= 16 */
+  int32_t window;           /* > 0: keys p-W+1..p visible; <= 0: unbounded */
+  int32_t use_rope;         /* NeoX RoPE at position p */
+  float rope_theta;
+  float rms_eps;
+  float softmax_scale;      /* 0 => 1/sqrt(head_dim) */
+  int32_t dtype;            /* FLINT_BF16 */
+  int32_t fp32_out;         /* out in float32 instead of bf16 */
+  int32_t reserved;         /* 0 */
+  int64_t q_stride;         /* elements between rows of q, k, v (their heads        */
+  int64_t k_stride;         /* contiguous, as in a fused projection), multiples of  */
+  int64_t v_stride;         /* 8; 0: H * D and Hk * D                               */
+} flint_decode_paged_params_t;
+
+/* Bytes of device workspace flint_attn_decode_paged needs on the current device
+ * (0 if the params are invalid); 256-byte aligned. It must be zero before its
+ * first use and serve no other entry point; every completed call leaves it ready
+ * for the next one, whatever that call's sizes, so it is cleared once and not
+ * per call. Calls that may overlap on the GPU (unordered streams) need one
+ * workspace each. */
+size_t flint_attn_decode_paged_workspace_bytes(const flint_decode_paged_params_t* params);
+
+/* flint_attn_decode over a paged cache. Sequence b has p = cache_lens[b] tokens
+ * cached; k_hat and v of the new token go into slot p as in
+ * flint_attn_paged_append, and the new query sees positions max(0, p-W+1) .. p
+ * (as the cache stores them, the new one included) plus the sink.
+ *   q [B, H, D], k, v [B, Hk, D] bfloat16 (raw projections); q_norm_w, k_norm_w
+ *   [D] bfloat16; sink [H] fp32; out [B, H, D] (bf16, or float32 with fp32_out);
+ *   lse [B, H] fp32 (natural log).
+ * Results are the same bits on every run with the same inputs on the same GPU. */
+flint_status_t flint_attn_decode_paged(const flint_decode_paged_params_t* params,
+                                       const void* q, const void* k, const void* v,
+                                       const void* q_norm_w, const void* k_norm_w,
+                                       const float* sink, const int32_t* cache_lens,
+                                       const int32_t* block_table, void* k_pages,
+                                       void* v_pages, const float* k_scale,
+                                       const float* v_scale, void* out, float* lse,
+                                       void* workspace, size_t workspace_bytes,
+                                       void* stream);
+
 /* Largest num_q_heads flint_attn_bwd_preprocess_static accepts. */
 #define FLINT_STATIC_MAX_HEADS 128
 
@@ -277,7 +397,8 @@ flint_status_t flint_attn_bwd_preprocess_static(const flint_attn_params_t* param
 /* Synchronises `stream`, reads and clears the device status word in
  * `workspace` (written by bounded device waits), and returns FLINT_OK or
  * FLINT_ERR_TIMEOUT (FLINT_ERR_INVALID_ARG for a flint_attn_decode workspace
- * whose call met an out-of-range cache_lens entry). It returns FLINT_ERR_CUDA
+ * whose call met an out-of-range cache_lens entry, and for the paged calls' device-side
+ * errors). It returns FLINT_ERR_CUDA
  * if the stream itself reports an error, or if a backward kernel found its
  * dynamic shared memory not 1024-byte aligned and did no work (its tiles need
  * that alignment; not expected). */

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "paged.cuh"
 #include "sm100_primitives.cuh"
 
 namespace flint {
@@ -55,7 +56,7 @@ const char* const kKernelNames[kNumKernelIds] = {
     "bwd_preprocess", "reduce_rows", "attn_bwd_dkv_sm100", "attn_bwd_dq_sm100",
     "attn_bwd_dq_fp32", "attn_bwd_dkv_fp32", "prologue_bwd", "convert_f16",
     "decode", "pad_fill", "absmax", "attn_fwd_x3_sm100", "attn_bwd_dkv_x3_sm100",
-    "attn_bwd_dq_x3_sm100"};
+    "attn_bwd_dq_x3_sm100", "paged_append", "decode_paged"};
 constexpr int kMaxSlots = 1 << 15;
 struct Prof {
   std::mutex mu;
@@ -540,6 +541,162 @@ extern "C" flint_status_t flint_attn_decode(const flint_decode_params_t* params,
   D.part_ml = at<float>(workspace, L.part_ml);
   D.out = out; D.lse = lse; D.status = status;
   return cuda_status(launch_decode(D, st));
+}
+
+// ------------------------------------------------------------------ paged cache
+namespace {
+// The descriptor's own checks; pointers are checked by check_paged_ptrs.
+flint_status_t resolve_cache(const flint_paged_cache_t& d, PagedCache* c) {
+  if (d.cache_dtype != FLINT_CACHE_BF16 && d.cache_dtype != FLINT_CACHE_E4M3)
+    return FLINT_ERR_INVALID_ARG;
+  if (d.num_pages < 1 || d.page_size < 1 || d.max_pages < 1 || d.num_kv_heads < 1)
+    return FLINT_ERR_INVALID_ARG;
+  if (d.head_dim != kHeadDim || d.page_size % 16 != 0) return FLINT_ERR_UNSUPPORTED;
+  if ((long long)d.max_pages * d.page_size > 0x7fffffffLL) return FLINT_ERR_INVALID_ARG;
+  const long long e = d.cache_dtype == FLINT_CACHE_E4M3 ? 1 : 2;
+  c->num_pages = d.num_pages; c->P = d.page_size; c->max_pages = d.max_pages;
+  c->Hk = d.num_kv_heads; c->e4m3 = d.cache_dtype == FLINT_CACHE_E4M3;
+  c->page_stride = d.page_stride; c->head_stride = d.head_stride;
+  c->token_stride = d.token_stride;
+  if (!d.page_stride && !d.head_stride && !d.token_stride) {
+    c->token_stride = kHeadDim;
+    c->head_stride = (long long)d.page_size * kHeadDim;
+    c->page_stride = (long long)d.num_kv_heads * d.page_size * kHeadDim;
+  }
+  // The bounds keep offsets in 64 bits and fit the tensor maps' 40-bit strides.
+  for (long long s : {c->page_stride, c->head_stride, c->token_stride})
+    if (s < kHeadDim || s >= (1LL << 38) || s * e % 16 != 0) return FLINT_ERR_INVALID_ARG;
+  c->table_stride = d.table_stride ? d.table_stride : d.max_pages;
+  if (c->table_stride < d.max_pages || c->table_stride >= (1LL << 32))
+    return FLINT_ERR_INVALID_ARG;
+  return FLINT_OK;
+}
+
+flint_status_t check_paged_ptrs(const int32_t* block_table, void* k_pages, void* v_pages,
+                                const float* k_scale, const float* v_scale, PagedCache* c) {
+  if (!block_table || !aligned(block_table, 4)) return FLINT_ERR_INVALID_ARG;
+  if (!k_pages || !aligned(k_pages, 16) || !v_pages || !aligned(v_pages, 16))
+    return FLINT_ERR_INVALID_ARG;
+  if (!aligned(k_scale, 4) || !aligned(v_scale, 4)) return FLINT_ERR_INVALID_ARG;
+  if (!c->e4m3 && (k_scale || v_scale)) return FLINT_ERR_INVALID_ARG;
+  c->table = block_table; c->k = k_pages; c->v = v_pages;
+  c->k_scale = k_scale; c->v_scale = v_scale;
+  return FLINT_OK;
+}
+
+// Row stride of a [rows, heads, D] bf16 tensor: 0 means contiguous.
+bool row_stride(int64_t given, long long heads, long long* out) {
+  *out = given ? given : heads * kHeadDim;
+  return *out >= heads * kHeadDim && *out < (1LL << 38) && *out % 8 == 0;
+}
+
+bool norm_rope_ok(float eps, int use_rope, float theta) {
+  if (!(std::isfinite(eps) && eps >= 0.f)) return false;
+  return !use_rope || (std::isfinite(theta) && theta > 0.f);
+}
+
+flint_status_t input_dtype_status(int dtype) {
+  if (dtype == FLINT_BF16) return FLINT_OK;
+  return dtype == FLINT_FP32 ? FLINT_ERR_UNSUPPORTED : FLINT_ERR_INVALID_ARG;
+}
+
+flint_status_t resolve_decode_paged(const flint_decode_paged_params_t* d, PagedDecodeLaunch* L,
+                                    size_t* ws_bytes) {
+  if (!d) return FLINT_ERR_INVALID_ARG;
+  flint_status_t s = input_dtype_status(d->dtype);
+  if (s != FLINT_OK) return s;
+  if ((s = resolve_cache(d->cache, &L->c)) != FLINT_OK) return s;
+  const int Hk = d->cache.num_kv_heads;
+  if (d->batch < 1 || d->num_q_heads < 1 || d->num_q_heads % Hk != 0 || d->reserved != 0)
+    return FLINT_ERR_INVALID_ARG;
+  if ((long long)d->batch * d->num_q_heads > 0x7fffffffLL / kHeadDim)
+    return FLINT_ERR_INVALID_ARG;
+  if (d->num_q_heads / Hk > 16) return FLINT_ERR_UNSUPPORTED;
+  if (!norm_rope_ok(d->rms_eps, d->use_rope, d->rope_theta)) return FLINT_ERR_INVALID_ARG;
+  if (!std::isfinite(d->softmax_scale) || d->softmax_scale < 0.f) return FLINT_ERR_INVALID_ARG;
+  if (!row_stride(d->q_stride, d->num_q_heads, &L->q_stride) ||
+      !row_stride(d->k_stride, Hk, &L->k_stride) || !row_stride(d->v_stride, Hk, &L->v_stride))
+    return FLINT_ERR_INVALID_ARG;
+  L->B = d->batch; L->H = d->num_q_heads; L->G = d->num_q_heads / Hk;
+  L->W = d->window > 0 ? d->window : 0;
+  L->rope = d->use_rope ? 1 : 0; L->out_f32 = d->fp32_out ? 1 : 0;
+  L->log2_theta = d->use_rope ? std::log2((double)d->rope_theta) : 0.0;
+  L->eps = d->rms_eps;
+  L->scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)kHeadDim);
+  *ws_bytes = decode_paged_layout(d->batch, Hk, sm_count(), nullptr);
+  return FLINT_OK;
+}
+}  // namespace
+
+extern "C" flint_status_t flint_attn_paged_append(
+    const flint_paged_append_params_t* params, const void* k, const void* v, const void* k_norm_w,
+    const int32_t* cu_new_lens, const int32_t* cache_lens, const int32_t* block_table,
+    void* k_pages, void* v_pages, const float* k_scale, const float* v_scale, int32_t* status,
+    void* stream) {
+  if (!params) return FLINT_ERR_INVALID_ARG;
+  PagedAppendLaunch L{};
+  flint_status_t s = input_dtype_status(params->dtype);
+  if (s != FLINT_OK) return s;
+  if ((s = resolve_cache(params->cache, &L.c)) != FLINT_OK) return s;
+  const int Hk = params->cache.num_kv_heads;
+  if (params->num_seqs < 1 || params->total_tokens < 0) return FLINT_ERR_INVALID_ARG;
+  if (!norm_rope_ok(params->rms_eps, params->use_rope, params->rope_theta) ||
+      !row_stride(params->k_stride, Hk, &L.k_stride) ||
+      !row_stride(params->v_stride, Hk, &L.v_stride))
+    return FLINT_ERR_INVALID_ARG;
+  const bool no_tokens = params->total_tokens == 0;
+  if ((!k && !no_tokens) || !aligned(k, 16) || (!v && !no_tokens) || !aligned(v, 16) ||
+      !k_norm_w || !aligned(k_norm_w, 16) || !cu_new_lens || !aligned(cu_new_lens, 4) ||
+      !cache_lens || !aligned(cache_lens, 4) || !status || !aligned(status, 256))
+    return FLINT_ERR_INVALID_ARG;
+  s = check_paged_ptrs(block_table, k_pages, v_pages, k_scale, v_scale, &L.c);
+  if (s != FLINT_OK) return s;
+  if (no_tokens) return FLINT_OK;
+  L.N = params->num_seqs; L.T = params->total_tokens; L.rope = params->use_rope ? 1 : 0;
+  L.log2_theta = L.rope ? std::log2((double)params->rope_theta) : 0.0;
+  L.eps = params->rms_eps;
+  L.k = static_cast<const __nv_bfloat16*>(k);
+  L.v = static_cast<const __nv_bfloat16*>(v);
+  L.wk = static_cast<const __nv_bfloat16*>(k_norm_w);
+  L.cu = cu_new_lens; L.lens = cache_lens; L.status = status;
+  return cuda_status(launch_paged_append(L, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+extern "C" size_t flint_attn_decode_paged_workspace_bytes(
+    const flint_decode_paged_params_t* params) {
+  PagedDecodeLaunch L{};
+  size_t n = 0;
+  return resolve_decode_paged(params, &L, &n) == FLINT_OK ? n : 0;
+}
+
+extern "C" flint_status_t flint_attn_decode_paged(
+    const flint_decode_paged_params_t* params, const void* q, const void* k, const void* v,
+    const void* q_norm_w, const void* k_norm_w, const float* sink, const int32_t* cache_lens,
+    const int32_t* block_table, void* k_pages, void* v_pages, const float* k_scale,
+    const float* v_scale, void* out, float* lse, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  PagedDecodeLaunch L{};
+  size_t need = 0;
+  flint_status_t s = resolve_decode_paged(params, &L, &need);
+  if (s != FLINT_OK) return s;
+  const void* vec16[] = {q, k, v, q_norm_w, k_norm_w, out};
+  for (const void* ptr : vec16)
+    if (!ptr || !aligned(ptr, 16)) return FLINT_ERR_INVALID_ARG;
+  if (!sink || !aligned(sink, 4) || !cache_lens || !aligned(cache_lens, 4) || !lse ||
+      !aligned(lse, 4))
+    return FLINT_ERR_INVALID_ARG;
+  s = check_paged_ptrs(block_table, k_pages, v_pages, k_scale, v_scale, &L.c);
+  if (s != FLINT_OK) return s;
+  if (!workspace || !aligned(workspace, 256)) return FLINT_ERR_INVALID_ARG;
+  if (workspace_bytes < need) return FLINT_ERR_WORKSPACE;
+  L.q = static_cast<const __nv_bfloat16*>(q);
+  L.k = static_cast<const __nv_bfloat16*>(k);
+  L.v = static_cast<const __nv_bfloat16*>(v);
+  L.wq = static_cast<const __nv_bfloat16*>(q_norm_w);
+  L.wk = static_cast<const __nv_bfloat16*>(k_norm_w);
+  L.sink = sink; L.lens = cache_lens; L.out = out; L.lse = lse;
+  L.status = static_cast<int*>(workspace);
+  return cuda_status(launch_decode_paged(L, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" flint_status_t flint_attn_check_status(void* workspace, void* stream) {

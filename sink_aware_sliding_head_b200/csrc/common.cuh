@@ -23,7 +23,8 @@ enum : int {
   kStatusTimeoutBwdKV = 2,
   kStatusTimeoutBwdQ = 4,
   kStatusSmemAlign = 8,        // dynamic shared memory not 1024-byte aligned
-  kStatusDecodeRange = 16,     // a decode cache_lens entry outside [0, cache_capacity)
+  kStatusDecodeRange = 16,     // a decode cache_lens entry outside [0, cache_capacity), or
+                               // a paged call's cache_lens or block_table entry out of range
   kStatusTimeoutSelftest = 32, // the bounded-wait self-test's wait ran out
 };
 
@@ -209,7 +210,7 @@ __device__ __forceinline__ void store8(float* p, const float (&f)[8]) {
 enum KernelId {
   kKPrologue = 0, kKWorklist, kKFwdSm100, kKFwdFp32, kKBwdPre, kKReduce, kKBwdDkvSm100,
   kKBwdDqSm100, kKBwdDqFp32, kKBwdDkvFp32, kKPrologueBwd, kKConvert, kKDecode, kKPadFill,
-  kKAbsmax, kKFwdX3, kKBwdDkvX3, kKBwdDqX3,
+  kKAbsmax, kKFwdX3, kKBwdDkvX3, kKBwdDqX3, kKPagedAppend, kKDecodePaged,
   kNumKernelIds
 };
 struct ProfScope {

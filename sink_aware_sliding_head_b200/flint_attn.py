@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(_HERE, "libflint_attn.so")
 
 FLINT_BF16 = 0
 FLINT_FP32 = 1
+CACHE_BF16 = 0
+CACHE_E4M3 = 1
 
 STATUS = {0: "FLINT_OK", 1: "FLINT_ERR_INVALID_ARG", 2: "FLINT_ERR_UNSUPPORTED",
           3: "FLINT_ERR_WORKSPACE", 4: "FLINT_ERR_CUDA", 5: "FLINT_ERR_TIMEOUT"}
@@ -30,7 +32,9 @@ EXPORTED = ["flint_attn_workspace_bytes", "flint_attn_fwd", "flint_attn_bwd",
             "flint_attn_profile_reset", "flint_attn_launch_count",
             "flint_attn_bwd_preprocess_static", "flint_attn_exp2_poly",
             "flint_attn_decode_workspace_bytes", "flint_attn_decode",
-            "flint_attn_fwd_padded", "flint_attn_bwd_padded", "flint_attn_selftest_wait"]
+            "flint_attn_fwd_padded", "flint_attn_bwd_padded", "flint_attn_selftest_wait",
+            "flint_attn_paged_append", "flint_attn_decode_paged_workspace_bytes",
+            "flint_attn_decode_paged"]
 
 
 class Params(ctypes.Structure):
@@ -67,6 +71,57 @@ class DecodeParams(ctypes.Structure):
         ("softmax_scale", ctypes.c_float),
         ("dtype", ctypes.c_int32),
         ("fp32_out", ctypes.c_int32),
+    ]
+
+
+class PagedCacheDesc(ctypes.Structure):
+    """Mirror of ``flint_paged_cache_t``."""
+    _fields_ = [
+        ("num_pages", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("cache_dtype", ctypes.c_int32),
+        ("page_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("token_stride", ctypes.c_int64),
+        ("table_stride", ctypes.c_int64),
+    ]
+
+
+class PagedAppendParams(ctypes.Structure):
+    """Mirror of ``flint_paged_append_params_t``."""
+    _fields_ = [
+        ("cache", PagedCacheDesc),
+        ("num_seqs", ctypes.c_int32),
+        ("total_tokens", ctypes.c_int32),
+        ("use_rope", ctypes.c_int32),
+        ("rope_theta", ctypes.c_float),
+        ("rms_eps", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
+    ]
+
+
+class DecodePagedParams(ctypes.Structure):
+    """Mirror of ``flint_decode_paged_params_t``."""
+    _fields_ = [
+        ("cache", PagedCacheDesc),
+        ("batch", ctypes.c_int32),
+        ("num_q_heads", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("use_rope", ctypes.c_int32),
+        ("rope_theta", ctypes.c_float),
+        ("rms_eps", ctypes.c_float),
+        ("softmax_scale", ctypes.c_float),
+        ("dtype", ctypes.c_int32),
+        ("fp32_out", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64),
+        ("k_stride", ctypes.c_int64),
+        ("v_stride", ctypes.c_int64),
     ]
 
 
@@ -127,6 +182,13 @@ def load_library(path: str = LIB_PATH):
     lib.flint_attn_decode_workspace_bytes.restype = sz
     lib.flint_attn_decode.argtypes = [DP] + [vp] * 11 + [vp, sz, vp]
     lib.flint_attn_decode.restype = ctypes.c_int
+    lib.flint_attn_paged_append.argtypes = [ctypes.POINTER(PagedAppendParams)] + [vp] * 12
+    lib.flint_attn_paged_append.restype = ctypes.c_int
+    PP = ctypes.POINTER(DecodePagedParams)
+    lib.flint_attn_decode_paged_workspace_bytes.argtypes = [PP]
+    lib.flint_attn_decode_paged_workspace_bytes.restype = sz
+    lib.flint_attn_decode_paged.argtypes = [PP] + [vp] * 15 + [sz, vp]
+    lib.flint_attn_decode_paged.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -368,6 +430,202 @@ def decode(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, k_cache, v_cache, wind
     if check_status:
         _check(lib.flint_attn_check_status(_ptr(workspace), st), "flint_attn_decode (device)")
     return out, lse
+
+
+# ---------------------------------------------------------------- paged KV cache
+# A pool may be head-major [pages, Hk, P, D] or any strided view of that shape
+# (a token-major pool transposed, one half of an interleaved K/V pool).
+
+def _on_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _vector(t, name, dtype, shape):
+    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} "
+                         f"{list(t.shape)}")
+
+
+def _rows(t, name, heads, D, n=None):
+    """Row stride of a bf16 [rows, heads, D] tensor whose rows are contiguous."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[1:] != (heads, D) or (n is not None and t.shape[0] != n):
+        raise ValueError(f"{name} must be [{'rows' if n is None else n}, {heads}, {D}], got "
+                         f"{list(t.shape)}")
+    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and heads > 1):
+        raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
+    if t.shape[0] <= 1:
+        return 0
+    if t.stride(0) < heads * D:                 # 0 would mean "contiguous" to the library
+        raise ValueError(f"{name}: rows must not overlap, got strides {t.stride()}")
+    return t.stride(0)
+
+
+def _paged_cache(k_pages, v_pages, block_table, rows, k_scale, v_scale) -> PagedCacheDesc:
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+        raise ValueError("k_pages and v_pages must be [pages, Hk, page_size, D] of one type, got "
+                         f"{k_pages.dtype} {list(k_pages.shape)} and {v_pages.dtype} "
+                         f"{list(v_pages.shape)}")
+    if k_pages.dtype == torch.bfloat16:
+        code = CACHE_BF16
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale belong to float8_e4m3fn caches")
+    elif k_pages.dtype == torch.float8_e4m3fn:
+        code = CACHE_E4M3
+    else:
+        raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
+    n, Hk, P, D = k_pages.shape
+    # the stride of an axis of length 1 is never used and may be anything
+    strides, other = ([D if t.shape[i] == 1 else t.stride(i) for i in range(3)]
+                      for t in (k_pages, v_pages))
+    if strides != other:
+        raise ValueError(f"k_pages and v_pages have different strides: {k_pages.stride()} and "
+                         f"{v_pages.stride()}")
+    if min(strides) < D or k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+        raise ValueError(f"slots must be {D} contiguous channels and not overlap, got strides "
+                         f"{k_pages.stride()}")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != rows \
+            or (block_table.shape[1] > 1 and block_table.stride(1) != 1) \
+            or (rows > 1 and block_table.stride(0) < block_table.shape[1]):
+        raise ValueError(f"block_table must be int32 [{rows}, max_pages] with contiguous rows, got "
+                         f"{block_table.dtype} {list(block_table.shape)}")
+    _vector(k_scale, "k_scale", torch.float32, (Hk,))
+    _vector(v_scale, "v_scale", torch.float32, (Hk,))
+    return PagedCacheDesc(n, P, block_table.shape[1], Hk, D, code, strides[0], strides[1],
+                          strides[2], block_table.stride(0) if rows > 1 else 0)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _paged_call(device, stream, fn):
+    """Runs ``fn(stream handle)`` with the tensors' device current and, for a given
+    stream, that stream current too, so that what fn allocates belongs to it."""
+    if device.type != "cuda":
+        raise ValueError(f"CUDA tensors expected, got {device}")
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        with torch.cuda.stream(stream):
+            return fn(stream.cuda_stream)
+    if device.index != torch.cuda.current_device():
+        with torch.cuda.device(device):
+            return fn(torch.cuda.current_stream().cuda_stream)
+    return fn(torch.cuda.current_stream().cuda_stream)
+
+
+def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, v_pages, use_rope,
+                 rope_theta, rms_eps=1e-6, k_scale=None, v_scale=None, status=None, stream=None,
+                 check_status=False):
+    """New tokens' keys and values into a paged cache, through ``flint_attn_paged_append``.
+
+    k, v [T,Hk,D] bf16 (raw projections; row stride free): rows cu_new_lens[b] ..
+    cu_new_lens[b+1] belong to sequence b and get positions cache_lens[b], ...;
+    keys are normalised and (``use_rope``) rotated on the way. cu_new_lens [N+1],
+    cache_lens [N] and block_table [N, max_pages] are int32 on the device; a
+    cache_lens of -1 leaves the sequence alone. k_pages, v_pages [pages, Hk,
+    page_size, D] bf16 or float8_e4m3fn (with per-head float32 scales [Hk]) are
+    written in place, whatever their page, head and token strides. ``status``: int32
+    [64] zeroed once by the caller, where device-side errors collect (a fresh one if
+    omitted); ``check_status`` synchronises and raises ``FlintError`` for them.
+    """
+    lib = load_library()
+    N = cache_lens.numel()
+    desc = _paged_cache(k_pages, v_pages, block_table, N, k_scale, v_scale)
+    Hk, D = desc.num_kv_heads, desc.head_dim
+    k_stride, v_stride = _rows(k, "k", Hk, D), _rows(v, "v", Hk, D, k.shape[0])
+    _vector(k_norm_w, "k_norm_w", torch.bfloat16, (D,))
+    _vector(cache_lens, "cache_lens", torch.int32, (N,))
+    _vector(cu_new_lens, "cu_new_lens", torch.int32, (N + 1,))
+    _vector(status, "status", torch.int32, (64,))
+    dev = k_pages.device
+    _on_device(dev, k=k, v=v, v_pages=v_pages, k_norm_w=k_norm_w, cu_new_lens=cu_new_lens,
+               cache_lens=cache_lens, block_table=block_table, k_scale=k_scale, v_scale=v_scale,
+               status=status)
+    p = PagedAppendParams(desc, N, k.shape[0], 1 if use_rope else 0, rope_theta, rms_eps,
+                          FLINT_BF16, k_stride, v_stride)
+
+    def call(st):
+        word = torch.zeros(64, dtype=torch.int32, device=dev) if status is None else status
+        _check(lib.flint_attn_paged_append(
+            ctypes.byref(p), _addr(k), _addr(v), _addr(k_norm_w), _addr(cu_new_lens),
+            _addr(cache_lens), _addr(block_table), _addr(k_pages), _addr(v_pages),
+            _addr(k_scale), _addr(v_scale), _addr(word), st), "flint_attn_paged_append")
+        if check_status:
+            _check(lib.flint_attn_check_status(_addr(word), st),
+                   "flint_attn_paged_append (device)")
+
+    _paged_call(dev, stream, call)
+
+
+def alloc_decode_paged_workspace(batch, num_q_heads, num_kv_heads, device=None) -> torch.Tensor:
+    """A zeroed workspace for ``decode_paged`` calls of up to this many rows.
+
+    One workspace serves any number of calls one after the other; calls that may
+    overlap on the GPU need one each.
+    """
+    with torch.cuda.device(device if device is not None else torch.cuda.current_device()):
+        p = DecodePagedParams(PagedCacheDesc(1, 16, 1, num_kv_heads, 128, CACHE_BF16), batch,
+                              num_q_heads)
+        n = load_library().flint_attn_decode_paged_workspace_bytes(ctypes.byref(p))
+        if n == 0:
+            raise FlintError(1, "flint_attn_decode_paged_workspace_bytes")
+        return torch.zeros(n, dtype=torch.uint8, device="cuda")
+
+
+def decode_paged(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_pages, v_pages,
+                 window, use_rope, rope_theta, rms_eps=1e-6, softmax_scale=0.0, k_scale=None,
+                 v_scale=None, out=None, lse=None, workspace=None, stream=None,
+                 check_status=False, fp32_out=False):
+    """One new token per sequence over a paged cache, through ``flint_attn_decode_paged``.
+
+    q [B,H,D], k, v [B,Hk,D] bf16 (raw projections of the new tokens; row strides
+    free); cache_lens [B] int32 on the device (-1: a row not in use, whose out and
+    lse stay as they are); block_table, k_pages, v_pages, k_scale, v_scale as for
+    ``paged_append``. The new key and value go into slot cache_lens[b]. Returns
+    (out [B,H,D], lse [B,H] fp32). ``workspace``: from
+    ``alloc_decode_paged_workspace``, kept between calls (a fresh one if omitted).
+    """
+    lib = load_library()
+    B = cache_lens.numel()
+    desc = _paged_cache(k_pages, v_pages, block_table, B, k_scale, v_scale)
+    Hk, D = desc.num_kv_heads, desc.head_dim
+    H = q.shape[1] if q.dim() == 3 else 0
+    strides = _rows(q, "q", H, D, B), _rows(k, "k", Hk, D, B), _rows(v, "v", Hk, D, B)
+    _vector(q_norm_w, "q_norm_w", torch.bfloat16, (D,))
+    _vector(k_norm_w, "k_norm_w", torch.bfloat16, (D,))
+    _vector(sink, "sink", torch.float32, (H,))
+    _vector(cache_lens, "cache_lens", torch.int32, (B,))
+    odt = torch.float32 if fp32_out else torch.bfloat16
+    _vector(out, "out", odt, (B, H, D))
+    _vector(lse, "lse", torch.float32, (B, H))
+    if workspace is not None:
+        _vector(workspace, "workspace", torch.uint8, (workspace.numel(),))
+    dev = k_pages.device
+    _on_device(dev, q=q, k=k, v=v, v_pages=v_pages, q_norm_w=q_norm_w, k_norm_w=k_norm_w,
+               sink=sink, cache_lens=cache_lens, block_table=block_table, k_scale=k_scale,
+               v_scale=v_scale, out=out, lse=lse, workspace=workspace)
+    p = DecodePagedParams(desc, B, H, window, 1 if use_rope else 0, rope_theta, rms_eps,
+                          softmax_scale, FLINT_BF16, 1 if fp32_out else 0, 0, *strides)
+
+    def call(st):
+        o = torch.empty((B, H, D), dtype=odt, device=dev) if out is None else out
+        ls = torch.empty((B, H), dtype=torch.float32, device=dev) if lse is None else lse
+        ws = alloc_decode_paged_workspace(B, H, Hk, dev) if workspace is None else workspace
+        _check(lib.flint_attn_decode_paged(
+            ctypes.byref(p), _addr(q), _addr(k), _addr(v), _addr(q_norm_w), _addr(k_norm_w),
+            _addr(sink), _addr(cache_lens), _addr(block_table), _addr(k_pages), _addr(v_pages),
+            _addr(k_scale), _addr(v_scale), _addr(o), _addr(ls), _addr(ws), ws.numel(), st),
+            "flint_attn_decode_paged")
+        if check_status:
+            _check(lib.flint_attn_check_status(_addr(ws), st), "flint_attn_decode_paged (device)")
+        return o, ls
+
+    return _paged_call(dev, stream, call)
 
 
 def exp2_poly(x: torch.Tensor) -> torch.Tensor:
