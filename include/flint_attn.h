@@ -281,7 +281,7 @@ typedef enum { FLINT_CACHE_BF16 = 0, FLINT_CACHE_E4M3 = 1 } flint_cache_dtype_t;
 typedef struct {
   int32_t num_pages;        /* pages in the pool, >= 1 */
   int32_t page_size;        /* P: slots per page, a multiple of 16 */
-  int32_t max_pages;        /* columns of block_table, >= 1; max_pages * P < 2^31 */
+  int32_t max_pages;        /* columns of block_table, >= 1; max_pages * P <= 2^30 */
   int32_t num_kv_heads;     /* Hk */
   int32_t head_dim;         /* D; must be 128 */
   int32_t cache_dtype;      /* flint_cache_dtype_t */

@@ -191,6 +191,30 @@ bool encode_3d(CUtensorMap* m, const void* base, int T, int heads, int box_heads
   return r == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+CUtensorMap paged_tensor_map(const PagedCache& c, const void* pool, int box, bool* ok) {
+  CUtensorMap m{};
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) { *ok = false; return m; }
+  const cuuint64_t e = c.e4m3 ? 1 : 2;
+  const cuuint32_t halves = c.e4m3 ? 1 : 2;
+  cuuint64_t dims[5] = {128 / e, (cuuint64_t)c.P, halves, (cuuint64_t)c.Hk,
+                        (cuuint64_t)c.num_pages};
+  cuuint64_t strides[4] = {c.token_stride * e, 128, c.head_stride * e, c.page_stride * e};
+  cuuint32_t boxd[5] = {(cuuint32_t)(128 / e), (cuuint32_t)box, halves, 1, 1};
+  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  const CUresult r = fn(&m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                        5, const_cast<void*>(pool), dims, strides, boxd, estr,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) *ok = false;
+  return m;
+}
+
+namespace {
+
 template <typename T>
 T* at(void* ws, size_t off) {
   return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
@@ -552,7 +576,7 @@ flint_status_t resolve_cache(const flint_paged_cache_t& d, PagedCache* c) {
   if (d.num_pages < 1 || d.page_size < 1 || d.max_pages < 1 || d.num_kv_heads < 1)
     return FLINT_ERR_INVALID_ARG;
   if (d.head_dim != kHeadDim || d.page_size % 16 != 0) return FLINT_ERR_UNSUPPORTED;
-  if ((long long)d.max_pages * d.page_size > 0x7fffffffLL) return FLINT_ERR_INVALID_ARG;
+  if ((long long)d.max_pages * d.page_size > (1LL << 30)) return FLINT_ERR_INVALID_ARG;
   const long long e = d.cache_dtype == FLINT_CACHE_E4M3 ? 1 : 2;
   c->num_pages = d.num_pages; c->P = d.page_size; c->max_pages = d.max_pages;
   c->Hk = d.num_kv_heads; c->e4m3 = d.cache_dtype == FLINT_CACHE_E4M3;
@@ -623,7 +647,7 @@ flint_status_t resolve_decode_paged(const flint_decode_paged_params_t* d, PagedD
   L->log2_theta = d->use_rope ? std::log2((double)d->rope_theta) : 0.0;
   L->eps = d->rms_eps;
   L->scale = d->softmax_scale > 0.f ? d->softmax_scale : 1.0f / std::sqrt((float)kHeadDim);
-  *ws_bytes = decode_paged_layout(d->batch, Hk, sm_count(), nullptr);
+  *ws_bytes = decode_paged_bytes(d->batch, Hk, sm_count());
   return FLINT_OK;
 }
 }  // namespace
@@ -696,7 +720,7 @@ extern "C" flint_status_t flint_attn_decode_paged(
   L.wk = static_cast<const __nv_bfloat16*>(k_norm_w);
   L.sink = sink; L.lens = cache_lens; L.out = out; L.lse = lse;
   L.status = static_cast<int*>(workspace);
-  return cuda_status(launch_decode_paged(L, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_decode_paged(L, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" flint_status_t flint_attn_check_status(void* workspace, void* stream) {

@@ -8,6 +8,7 @@
 // (strides in elements), so head-major [pages, Hk, P, D] and token-major
 // [pages, P, Hk, D] pools, or K and V interleaved in one tensor, are one case.
 #pragma once
+#include <cuda.h>
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -102,14 +103,24 @@ __device__ __forceinline__ uint2 pack_e4m3_row(const float (&x)[8], float scale)
 __device__ __forceinline__ float e4m3_to_f32(uint32_t bits) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)bits, __NV_E4M3)));
 }
-// Stores the lane's channels 8l .. 8l+7 of a row at element offset off.
-__device__ __forceinline__ void store_row(const PagedCache& c, void* pool, long long off,
-                                          const float (&x)[8], float scale) {
+// Stores the lane's channels 8l .. 8l+7 of a row at element offset off (e4m3:
+// the first 8 bytes of u).
+__device__ __forceinline__ void store_bits(const PagedCache& c, void* pool, long long off,
+                                           uint4 u) {
   const int l = threadIdx.x & 15;
   if (c.e4m3)
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + off + 8 * l) = pack_e4m3_row(x, scale);
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + off + 8 * l) = make_uint2(u.x, u.y);
   else
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + off + 8 * l) = pack_bf16_row(x);
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + off + 8 * l) = u;
+}
+__device__ __forceinline__ void store_row(const PagedCache& c, void* pool, long long off,
+                                          const float (&x)[8], float scale) {
+  if (c.e4m3) {
+    const uint2 u = pack_e4m3_row(x, scale);
+    store_bits(c, pool, off, make_uint4(u.x, u.y, 0, 0));
+  } else {
+    store_bits(c, pool, off, pack_bf16_row(x));
+  }
 }
 
 // ------------------------------------------------------------------ launchers
@@ -139,7 +150,11 @@ struct PagedDecodeLaunch {
   int* status;
 };
 // Bytes of workspace for B rows and Hk KV heads on a GPU of num_sms SMs.
-size_t decode_paged_layout(int B, int Hk, int num_sms, void* layout);
-cudaError_t launch_decode_paged(const PagedDecodeLaunch& a, cudaStream_t st);
+size_t decode_paged_bytes(int B, int Hk, int num_sms);
+cudaError_t launch_decode_paged(const PagedDecodeLaunch& a, int num_sms, cudaStream_t st);
+// A pool as [page][head][half][slot][channels] with 128-byte rows (bf16: two
+// halves of 64 channels, e4m3: one of 128) and 128-byte swizzle; a box is `box`
+// slots of one head of one page, both halves. ok is cleared on failure.
+CUtensorMap paged_tensor_map(const PagedCache& c, const void* pool, int box, bool* ok);
 
 }  // namespace flint
