@@ -16,15 +16,20 @@
 //     (m, l, O) and the last of a pair's segments to finish joins them. The plan
 //     is made on the device by every block (a scan over lens), so a captured
 //     call follows its lengths and nothing but lens decides who sums what.
-//   * Loads. One warp streams K and V of the range through a ring of shared
-//     memory with TMA, across segment borders, so that the ring fills while the
-//     other warps finish one segment and start the next. A tensor map in five
+//   * Loads. Four warps stream K and V of the range, a block each in turn, through
+//     a ring of shared memory with TMA, across segment borders, so that the ring
+//     fills while the math warps finish one segment and start the next. (Issuing a
+//     copy costs a warp 130 cycles or more: over 16-slot pages of e4m3 one warp
+//     alone took as long as its blocks' share of the HBM bandwidth twice over.) A tensor map in five
 //     dimensions (64 channels, slot, channel half, head, page) takes any page,
 //     head and token strides; a box is the largest power of two of slots that
-//     divides the page, at most 64, so no box crosses a page.
-//   * Math. Eight warps in two groups of four take the blocks in turn, 16 keys a
-//     warp, on mma.sync m16n8k16 with FP32 accumulation. Eight query heads at a
-//     time: S takes q as two 16-bit parts, hi in rows 0-7 and lo in rows 8-15 of
+//     divides the page, at most 64, so no box crosses a page. With the rings of
+//     148 SMs full, 19 MB are in flight and any load waits ~3 us behind them, so
+//     the first of these warps brings everything else a segment needs (the q rows, the new
+//     row, the page of its slot, scales, sinks) up to four segments ahead.
+//   * Math. Eight warps take the blocks in turn, 32 keys and eight query heads a
+//     warp (up to 8 heads: four pairs of warps, a block each; 9 to 16: two groups
+//     of four), on mma.sync m16n8k16 with FP32 accumulation. S takes q as two 16-bit parts, hi in rows 0-7 and lo in rows 8-15 of
 //     one A operand, so q keeps 16 bits of mantissa (22 over e4m3, whose
 //     products run in fp16) and the LSE stays exact to ~1e-6. O^T += V^T P^T
 //     has the heads as the MMA's N, and the P fragment that a lane holds is
@@ -42,44 +47,63 @@ namespace flint {
 namespace {
 
 constexpr int kBlk = 64;                     // positions per unit of work
+constexpr int kKeys = 32;                    // of a block, per warp
 constexpr int kMathWarps = 8;
+constexpr int kLoadWarps = 4;                // block n is loaded by warp n % 4
 constexpr int kMathThreads = 32 * kMathWarps;
-constexpr int kThreads = kMathThreads + 32;  // + the loading warp
+constexpr int kThreads = kMathThreads + 32 * kLoadWarps;
 constexpr int kMergeRow = kHeadDim + 4;      // O, m, l (and two unused): rows stay 16-byte aligned
+constexpr int kSegs = 4;                     // segments described ahead
+constexpr int kLensKept = 512;               // rows whose lens a block keeps
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;             // log2 units
 
-// Shared memory: [ring | merge rows of the 8 warps (q rows before that) | Small].
-// NG: query heads in groups of 8 (1: G <= 8, 2: G <= 16).
-template <int NG, bool kF8>
-struct Cfg {
-  static constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
-  static constexpr int kStageBytes = 2 * kBlk * kRowBytes;          // K, then V
-  static constexpr int kMergeBytes = kMathWarps * 8 * NG * kMergeRow * 4;
-  // Even: the two groups of warps take the blocks in turn, so each stage then
-  // belongs to one group, which sees every phase of its barriers. With an odd
-  // ring a group's parity wait could be two phases behind and pass too early.
-  static constexpr int kStages = (NG == 1 ? 4 : 4) * (kF8 ? 2 : 1);
-  static_assert(kStages % 2 == 0 && kStages <= 16, "see above");
-  // P = 2^(s - m + bias): fp16 P starts at 2^-24, so its rows are lifted
-  static constexpr float kBias = kF8 ? 6.f : 0.f;
+// What the math warps need of a segment, brought by the loading warp.
+struct __align__(16) Seg {
+  __nv_bfloat16 q[16 * kHeadDim], k[kHeadDim], v[kHeadDim];    // raw rows (k, v: last segment)
+  float sink[16], ks, vs;
+  long long dst;                             // the new token's slot (KV head 0), -1: no page
+  int b, g;                                  // b = -1: no more segments
+  int blk, len, n;                           // blocks blk .. blk + len - 1 of the pair's n
+  int p, lo, first;                          // of the row, as in Range
+  int c0, c1;                                // the ranges that share the pair
 };
 struct Small {
-  uint64_t full[16], empty[16];
+  uint64_t full[16], empty[16], seg_full[kSegs], seg_empty[kSegs];
   int bad[16];                               // the stage lacks a page
   float cs[kHeadDim / 2], sn[kHeadDim / 2];
   float knew[kHeadDim], vnew[kHeadDim];      // the new row as the cache stores it, times scale
   uint4 kbits[16], vbits[16];                // and its bits, a lane's channels each
   float snew[16];                            // its scores, log2 units
   long long scan[kThreads / 32], start_off;
-  int start_b, no_page, abort_flag, last;
+  int start_b, abort_flag, last[2];
+  int lens[kLensKept];
 };
+// Shared memory: [ring | merge rows of the 8 warps (q rows before that) | q
+// fragments | segments | Small].
+// NG: query heads in groups of 8 (1: G <= 8, 2: G <= 16).
 template <int NG, bool kF8>
-constexpr int smem_bytes() {
-  return Cfg<NG, kF8>::kStages * Cfg<NG, kF8>::kStageBytes + Cfg<NG, kF8>::kMergeBytes +
-         (int)sizeof(Small) + 1024;
-}
+struct Cfg {
+  static constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
+  static constexpr int kStageBytes = 2 * kBlk * kRowBytes;          // K, then V
+  // A multiple of the groups: the groups take the blocks in turn, so each stage
+  // then belongs to one group, which sees every phase of its barriers. In any
+  // other ring a group's parity wait could be two phases behind and pass early.
+  static constexpr int kGroupWarps = 2 * NG, kGroups = kMathWarps / kGroupWarps;
+  static constexpr int kStages = kF8 ? 8 : 4;
+  static_assert(kStages % kGroups == 0 && kStages <= 16, "see above");
+  static_assert(kStages % kLoadWarps == 0, "a stage belongs to one loading warp");
+  static constexpr int kMergeBytes = kMathWarps * 8 * kMergeRow * 4;
+  static constexpr int kFragBytes = NG * 8 * 32 * 16;
+  static constexpr int kOffMerge = kStages * kStageBytes;
+  static constexpr int kOffFrag = kOffMerge + kMergeBytes;
+  static constexpr int kOffSegs = kOffFrag + kFragBytes;
+  static constexpr int kOffSmall = kOffSegs + kSegs * (int)sizeof(Seg);
+  static constexpr int kSmemBytes = kOffSmall + (int)sizeof(Small) + 1024;   // + alignment
+  // P = 2^(s - m + bias): fp16 P starts at 2^-24, so its rows are lifted
+  static constexpr float kBias = kF8 ? 6.f : 0.f;
+};
 
 struct Args {
   PagedDecodeLaunch a;
@@ -95,45 +119,51 @@ struct Range {                               // what a row's new query reads of 
   int p, lo;                                 // cached positions lo .. p-1
   int first, n;                              // 64-position blocks; n = 0: nothing to do
 };
-__device__ __forceinline__ Range row_range(const PagedDecodeLaunch& a, int b) {
+__device__ __forceinline__ Range row_range(const PagedDecodeLaunch& a, int p) {
   Range r;
-  r.p = __ldg(a.lens + b);
-  r.lo = a.W > 0 ? max(0, r.p - a.W + 1) : 0;
+  r.p = p;
+  r.lo = a.W > 0 ? max(0, p - a.W + 1) : 0;
   r.first = r.lo / kBlk;
   r.n = 0;
-  if (r.p >= 0 && r.p < (long long)a.c.P * a.c.max_pages)
-    r.n = r.p > r.lo ? (r.p - 1) / kBlk - r.first + 1 : 1;   // 1: only the new token
+  if (p >= 0 && p < (long long)a.c.P * a.c.max_pages)
+    r.n = p > r.lo ? (p - 1) / kBlk - r.first + 1 : 1;   // 1: only the new token
   return r;
 }
 // First unit of block i's range, and the block whose range holds unit u.
+// (Quotients of numbers below 2^32 take the short division.)
+__device__ __forceinline__ long long quotient(long long x, long long y) {
+  return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+}
 __device__ __forceinline__ long long range_begin(long long units, int i, int blocks) {
-  return units * i / blocks;
+  return quotient(units * i, blocks);
 }
 __device__ __forceinline__ int range_of(long long units, long long u, int blocks) {
-  return (int)(((u + 1) * blocks - 1) / units);
+  return (int)quotient((u + 1) * blocks - 1, units);
 }
 
-// The segments of one block's range, in order; the same for every thread.
+// The segments of one block's range, in order.
 struct Walk {
-  int b;                                     // row
+  int b, b0;                                 // row; the first whose lens is kept
   long long off, left;                       // unit within the row's n * Hk; units left
   Range r;
-  // the segment: KV head g, blocks blk .. blk + len - 1 of the pair's r.n
-  int g, blk, len;
-  __device__ bool next(const PagedDecodeLaunch& a, bool first) {
-    if (!first) {
-      off += len;
-      left -= len;
-      if (left == 0) return false;
-      if (off == (long long)r.n * a.c.Hk) {
-        off = 0;
-        do r = row_range(a, ++b);            // ends: left > 0 units lie in later rows
-        while (r.n == 0);
-      }
-    }
-    g = (int)(off / r.n);
+  int g, blk, len;                           // the segment: KV head, blocks of the pair's r.n
+  __device__ void cut() {
+    g = (int)quotient(off, r.n);
     blk = (int)(off - (long long)g * r.n);
     len = (int)min((long long)(r.n - blk), left);
+  }
+  __device__ bool next(const PagedDecodeLaunch& a, const int* lens) {
+    off += len;
+    left -= len;
+    if (left == 0) return false;
+    if (off == (long long)r.n * a.c.Hk) {
+      off = 0;
+      do {                                   // ends: left > 0 units lie in later rows
+        ++b;
+        r = row_range(a, b - b0 < kLensKept ? lens[b - b0] : __ldg(a.lens + b));
+      } while (r.n == 0);
+    }
+    cut();
     return true;
   }
 };
@@ -147,24 +177,40 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, 
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(slot), "r"(head), "r"(page)
       : "memory");
 }
+// Untiled copy of bytes (a multiple of 16, both addresses 16-byte aligned).
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void math_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kMathThreads) : "memory");
 }
+__device__ __forceinline__ bool math_sync_and(bool x) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\tselp.b32 %0, 1, 0, q;\n\t}"
+      : "=r"(r) : "r"((int)x), "n"(kMathThreads) : "memory");
+  return r != 0;
+}
 template <bool kF8>
-__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint4 a, uint32_t b0,
                                          uint32_t b1) {
   if constexpr (kF8)
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
   else
     asm volatile(
         "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 template <bool kTrans>
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
@@ -198,6 +244,19 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uin
   }
 }
 
+// Channels d .. d+3 of an output row from the joined sums, and its LSE once.
+__device__ __forceinline__ void write_out(const PagedDecodeLaunch& a, long long row, int d,
+                                          float4 O, float M, float L) {
+  const float inv = 1.f / L;
+  if (a.out_f32)
+    *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kHeadDim + d) =
+        make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
+  else
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kHeadDim + d) =
+        make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
+  if (d == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+}
+
 // ------------------------------------------------------------------ the kernel
 template <int NG, bool kF8>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -207,15 +266,21 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* merge = reinterpret_cast<float*>(smem + C::kStages * C::kStageBytes);
-  Small& sm = *reinterpret_cast<Small*>(smem + C::kStages * C::kStageBytes + C::kMergeBytes);
+  float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
+  uint4* frag = reinterpret_cast<uint4*>(smem + C::kOffFrag);
+  Seg* segs = reinterpret_cast<Seg*>(smem + C::kOffSegs);
+  Small& sm = *reinterpret_cast<Small*>(smem + C::kOffSmall);
   const PagedDecodeLaunch& a = A.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == kMathThreads) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
-      mbar_init(smem_u32(&sm.empty[s]), kMathWarps / 2);
+      mbar_init(smem_u32(&sm.empty[s]), C::kGroupWarps);
+    }
+    for (int s = 0; s < kSegs; ++s) {
+      mbar_init(smem_u32(&sm.seg_full[s]), 1);
+      mbar_init(smem_u32(&sm.seg_empty[s]), kMathWarps);
     }
     sm.abort_flag = 0;
     fence_mbar_init();
@@ -224,15 +289,16 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 
   // ---- the plan: all units, and where this block's range begins
-  long long units;
+  long long units, left;
   int blocks;                                // that have a range: no range is empty
-  Walk w;
   {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
-      const Range r = row_range(a, b);
+      const int p = __ldg(a.lens + b);
+      const Range r = row_range(a, p);
+      if (a.B <= kLensKept) sm.lens[b] = p;
       sum += r.n;
       if (r.n == 0 && r.p != -1 && blockIdx.x == 0) atomicOr(a.status, kStatusDecodeRange);
     }
@@ -245,20 +311,22 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (lane == 31) sm.scan[warp] = incl;
     __syncthreads();
     long long before = incl - sum, total = 0;
+#pragma unroll
     for (int i = 0; i < kThreads / 32; ++i) {
       if (i < warp) before += sm.scan[i];
       total += sm.scan[i];
     }
     units = total * a.c.Hk;
     blocks = (int)min((long long)gridDim.x, units);
-    const bool idle = (int)blockIdx.x >= blocks;
-    const long long u0 = idle ? units : range_begin(units, blockIdx.x, blocks);
-    w.left = idle ? 0 : range_begin(units, blockIdx.x + 1, blocks) - u0;
+    if ((int)blockIdx.x >= blocks) return;
+    const long long u0 = range_begin(units, blockIdx.x, blocks);
+    left = range_begin(units, blockIdx.x + 1, blocks) - u0;
     long long at = u0 - before * a.c.Hk;
     if (at >= 0 && at < sum * a.c.Hk) {
       int b = b0;
       for (;; ++b) {                         // ends inside b0 .. b1-1: at < sum * Hk
-        const long long n = (long long)row_range(a, b).n * a.c.Hk;
+        const int p = a.B <= kLensKept ? sm.lens[b] : __ldg(a.lens + b);
+        const long long n = (long long)row_range(a, p).n * a.c.Hk;
         if (at < n) break;
         at -= n;
       }
@@ -266,38 +334,111 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       sm.start_off = at;
     }
     __syncthreads();
-    if (w.left == 0) return;
-    w.b = sm.start_b;
-    w.off = sm.start_off;
-    w.r = row_range(a, w.b);
+    if (a.B > kLensKept) {                   // the rows from the range's first
+      for (int i = threadIdx.x; i < min(kLensKept, a.B - sm.start_b); i += kThreads)
+        sm.lens[i] = __ldg(a.lens + sm.start_b + i);
+      __syncthreads();
+    }
   }
   const WaitCtx wc{&sm.abort_flag, a.status, kStatusTimeoutFwd};
 
-  if (warp == kMathWarps) {
+  if (warp >= kMathWarps) {
     // ---------------------------------------------------------------- loads
-    const int nbox = kBlk / A.box;
+    const int nbox = kBlk / A.box;                             // 1, 2 or 4 boxes a block
     const uint32_t box_bytes = (uint32_t)A.box * C::kRowBytes;
-    uint32_t n = 0;
+    const uint32_t lw = warp - kMathWarps;                     // takes blocks n % 4 == lw
+    uint32_t n = 0, k = 0, issued = 0;                         // issued: its last block + 1
     bool ok = true;
-    for (bool more = w.next(a, true); more && ok; more = w.next(a, false)) {
-      const int32_t* row = a.c.table + w.b * a.c.table_stride;
-      // lane i < nbox holds the page of box i of the coming block
-      auto page_of = [&](int blk) {
-        const int pos = (w.r.first + blk) * kBlk + lane * A.box;
-        const bool need = lane < nbox && pos + A.box > w.r.lo && pos < w.r.p;
-        return need ? __ldg(row + pos / a.c.P) : -2;          // -2: no visible slot
-      };
-      int page = page_of(w.blk);
-      for (int j = 0; j < w.len && ok; ++j, ++n) {
-        const int cur = page;
-        if (j + 1 < w.len) page = page_of(w.blk + j + 1);
-        const int s = n % C::kStages;
-        if (n >= C::kStages)
-          ok = mbar_wait_warp(smem_u32(&sm.empty[s]), (n / C::kStages - 1) & 1, wc);
+    Walk w;
+    w.b = sm.start_b;
+    w.b0 = a.B > kLensKept ? w.b : 0;
+    w.off = sm.start_off;
+    w.left = left;
+    w.r = row_range(a, sm.lens[w.b - w.b0]);
+    w.cut();
+    // The table is read 32 boxes at a time and ahead: lane i holds the page and
+    // slot of box at + i of a segment (-2: nothing visible; -1: a bad page).
+    struct Box { int page, slot; };
+    auto fetch = [&](const Walk& v, int at) {
+      const int i = at + lane, pos = (v.r.first + v.blk) * kBlk + i * A.box;
+      const bool need = i < v.len * nbox && pos + A.box > v.r.lo && pos < v.r.p;
+      const int col = pos / a.c.P;
+      const int32_t* row = a.c.table + v.b * a.c.table_stride;
+      return Box{need ? max(__ldg(row + col), -1) : -2, pos - col * a.c.P};
+    };
+    // What a segment needs besides keys, requested one segment ahead.
+    struct Ahead { Box box; long long dst; float sink, ks, vs; };
+    auto look = [&](const Walk& v) {
+      Ahead h;
+      h.box = fetch(v, 0);
+      h.dst = slot_offset(a.c, v.b, v.r.p);
+      h.sink = lane < a.G ? __ldg(a.sink + v.g * a.G + lane) : 0.f;
+      h.ks = kF8 && a.c.k_scale ? __ldg(a.c.k_scale + v.g) : 1.f;
+      h.vs = kF8 && a.c.v_scale ? __ldg(a.c.v_scale + v.g) : 1.f;
+      return h;
+    };
+    Ahead h = look(w);
+    while (true) {
+      // ---- describe the segment
+      Seg& sg = segs[k % kSegs];
+      if (lw == 0 && k >= kSegs)
+        ok = mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc);
+      if (!ok) break;
+      const bool owner = w.blk + w.len == w.r.n;
+      if (lw == 0 && lane < 16) sg.sink[lane] = h.sink;
+      if (lw == 0 && lane == 0) {
+        sg.ks = h.ks;
+        sg.vs = h.vs;
+        sg.dst = h.dst;
+        sg.b = w.b;
+        sg.g = w.g;
+        sg.blk = w.blk;
+        sg.len = w.len;
+        sg.n = w.r.n;
+        sg.p = w.r.p;
+        sg.lo = w.r.lo;
+        sg.first = w.r.first;
+        if (w.len < w.r.n) {
+          const long long u_pair = range_begin(units, blockIdx.x + 1, blocks) - w.left - w.blk;
+          sg.c0 = range_of(units, u_pair, blocks);
+          sg.c1 = range_of(units, u_pair + w.r.n - 1, blocks);
+        }
+      }
+      __syncwarp();
+      if (lw == 0 && lane == 0) {
+        const uint32_t bar = smem_u32(&sm.seg_full[k % kSegs]);
+        const uint32_t q_bytes = (uint32_t)a.G * kHeadDim * 2, row = kHeadDim * 2;
+        mbar_arrive_expect_tx(bar, q_bytes + (owner ? 2 * row : 0));
+        bulk_load(smem_u32(sg.q), a.q + w.b * a.q_stride + (long long)w.g * a.G * kHeadDim,
+                  q_bytes, bar);
+        if (owner) {
+          bulk_load(smem_u32(sg.k), a.k + w.b * a.k_stride + w.g * kHeadDim, row, bar);
+          bulk_load(smem_u32(sg.v), a.v + w.b * a.v_stride + w.g * kHeadDim, row, bar);
+        }
+      }
+      ++k;
+      // ---- its keys
+      Walk nx = w;
+      const bool more = nx.next(a, sm.lens);
+      Box cur = h.box, ahead = fetch(w, 32);
+      if (more) h = look(nx);
+      int batch = 0;
+      for (int j = (int)((lw - n) & (kLoadWarps - 1)); j < w.len; j += kLoadWarps) {
+        const int i = j * nbox;                                // the block's first box
+        if (i / 32 != batch) {                                 // a turn has at most 16 boxes
+          cur = ahead;
+          ahead = fetch(w, 32 * (++batch + 1));
+        }
+        const uint32_t u = n + j;
+        const int s = u % C::kStages;
+        if (u >= C::kStages)
+          ok = mbar_wait_warp(smem_u32(&sm.empty[s]), (u / C::kStages - 1) & 1, wc);
         if (!ok) break;
-        const int pos = (w.r.first + w.blk + j) * kBlk + lane * A.box;
-        const bool need = lane < nbox && pos + A.box > w.r.lo && pos < w.r.p;
-        const bool good = need && (unsigned)cur < (unsigned)a.c.num_pages;
+        issued = u + 1;
+        const int page = __shfl_sync(0xffffffffu, cur.page, (i + lane) & 31);
+        const int slot = __shfl_sync(0xffffffffu, cur.slot, (i + lane) & 31);
+        const bool need = lane < nbox && page != -2;
+        const bool good = need && (unsigned)page < (unsigned)a.c.num_pages;
         const unsigned good_mask = __ballot_sync(0xffffffffu, good);
         const unsigned bad_mask = __ballot_sync(0xffffffffu, need && !good);
         const uint32_t full = smem_u32(&sm.full[s]);
@@ -309,223 +450,218 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         __syncwarp();
         if (good) {
           const uint32_t dst = smem_u32(smem + s * C::kStageBytes) + lane * box_bytes;
-          const int slot = pos % a.c.P;
-          tma_load_5d(dst, &tm_k, full, slot, w.g, cur);
-          tma_load_5d(dst + kBlk * C::kRowBytes, &tm_v, full, slot, w.g, cur);
+          tma_load_5d(dst, &tm_k, full, slot, w.g, page);
+          tma_load_5d(dst + kBlk * C::kRowBytes, &tm_v, full, slot, w.g, page);
         }
         __syncwarp();
+      }
+      n += w.len;
+      if (!ok || !more) break;
+      w = nx;
+    }
+    const uint32_t described = k;
+    if (ok && lw == 0) {                                                  // the end
+      if (k >= kSegs)
+        ok = mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc);
+      if (ok && lane == 0) {
+        segs[k % kSegs].b = -1;
+        mbar_arrive(smem_u32(&sm.seg_full[k % kSegs]));
       }
     }
     // Every copy has landed before the block can exit (immediate unless a wait
     // ran out: the math warps saw each one).
     volatile int no_abort = 0;
     const WaitCtx drain{&no_abort, a.status, kStatusTimeoutFwd};
-    for (uint32_t i = n > C::kStages ? n - C::kStages : 0; i < n; ++i)
-      mbar_wait_warp(smem_u32(&sm.full[i % C::kStages]), (i / C::kStages) & 1, drain);
+    for (uint32_t u = issued > C::kStages ? issued - C::kStages : 0; u < issued; ++u)
+      if (u % kLoadWarps == lw)
+        mbar_wait_warp(smem_u32(&sm.full[u % C::kStages]), (u / C::kStages) & 1, drain);
+    for (uint32_t i = described > kSegs ? described - kSegs : 0; i < described; ++i)
+      if (lw == 0 && (i + kSegs > k || !ok))                   // not yet described anew
+        mbar_wait_warp(smem_u32(&sm.seg_full[i % kSegs]), (i / kSegs) & 1, drain);
     return;
   }
 
   // ------------------------------------------------------------------ math
   const int gid = lane >> 2, tig = lane & 3;
   const int half = threadIdx.x >> 4, l16 = threadIdx.x & 15;   // 16 half-warps
-  const int group = warp >> 2;                                 // takes stages n % 2 == group
-  const int key0 = 16 * (warp & 3);                            // of the block
+  const int group = warp / C::kGroupWarps;                     // takes blocks n % kGroups == group
+  const int key0 = kKeys * (warp & 1);                         // of the block
+  const int t8 = NG == 1 ? 0 : 8 * ((warp >> 1) & 1);          // the warp's first query head
   const uint32_t ring = smem_u32(smem);
-  // the warp's 16 keys lie in one box (boxes have 16, 32 or 64 slots)
-  const uint32_t key_base = (uint32_t)(key0 / A.box) * A.box * C::kRowBytes +
-                            (uint32_t)(key0 % A.box) * 128;
+  // 16 of the warp's keys lie in one box (boxes have 16, 32 or 64 slots)
+  uint32_t chunk_at[2];
+#pragma unroll
+  for (int c = 0; c < 2; ++c)
+    chunk_at[c] = (uint32_t)((key0 + 16 * c) / A.box) * A.box * C::kRowBytes +
+                  (uint32_t)((key0 + 16 * c) % A.box) * 128;
   const uint32_t half_bytes = (uint32_t)A.box * 128;           // bf16: channels 64..127
+  float wq[8], wk[8];
+  load8(a.wq + 8 * l16, wq);
+  load8(a.wk + 8 * l16, wk);
   uint32_t n = 0;
   int last_b = -1;
   bool ok = true;
+  // Partials, with their pair's ranges c0 .. c1: of a pair that began in an
+  // earlier range (first), and of one that goes on in a later range (last).
+  struct Part { int b, g, c0, c1; } first_part{-1, 0, 0, 0}, last_part{-1, 0, 0, 0};
 
-  for (bool more = w.next(a, true); more; more = w.next(a, false)) {
-    const bool owner = w.blk + w.len == w.r.n;                 // this segment has the new token
-    const int h0 = w.g * a.G;
-    const float ks = kF8 && a.c.k_scale ? __ldg(a.c.k_scale + w.g) : 1.f;
-    const float vs = kF8 && a.c.v_scale ? __ldg(a.c.v_scale + w.g) : 1.f;
+  for (uint32_t k = 0;; ++k) {
+    const Seg& sg = segs[k % kSegs];
+    if (ok) ok = mbar_wait_warp(smem_u32(&sm.seg_full[k % kSegs]), (k / kSegs) & 1, wc);
+    if (ok && a.rope && sg.b >= 0 && sg.b != last_b && threadIdx.x < kHeadDim / 2)
+      rope_cos_sin(sg.p, threadIdx.x, a.rope_pow, &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
+    if (!math_sync_and(ok)) break;                             // table; merge area free
+    if (sg.b < 0) break;
+    last_b = sg.b;
+    const int len = sg.len, p = sg.p, lo = sg.lo;
+    const bool owner = sg.blk + len == sg.n;                   // this segment has the new token
+    const float ks = sg.ks;
 
     // ---- q rows (half-warps 0 .. G-1) and, in the last segment, the new row
-    float x[8] = {}, wt[8] = {};
-    uint4 uk{}, uv{}, uw{};
-    const bool has_q = half < a.G;
-    if (has_q) {
-      load8(a.q + w.b * a.q_stride + (long long)(h0 + half) * kHeadDim + 8 * l16, x);
-      load8(a.wq + 8 * l16, wt);
-    }
-    long long dst = 0;                                         // the new row's slot, -1: no page
-    if (owner && warp == kMathWarps - 1) {                     // both half-warps the same row
-      dst = slot_offset(a.c, w.b, w.r.p);
-      uk = *reinterpret_cast<const uint4*>(a.k + w.b * a.k_stride + w.g * kHeadDim + 8 * l16);
-      uv = *reinterpret_cast<const uint4*>(a.v + w.b * a.v_stride + w.g * kHeadDim + 8 * l16);
-      uw = *reinterpret_cast<const uint4*>(a.wk + 8 * l16);
-    }
-    if (a.rope && w.b != last_b && threadIdx.x < kHeadDim / 2)
-      rope_cos_sin(w.r.p, threadIdx.x, a.log2_theta, &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
-    last_b = w.b;
-    math_sync();                                               // table; merge area free
-    row_prologue(x, wt, sm.cs, sm.sn, a.rope, a.eps);
     float (*qs)[kHeadDim] = reinterpret_cast<float (*)[kHeadDim]>(merge);
-    if (half < 8 * NG) {                                       // zero past G
+    if (half < 8 * NG) {                                       // whole warps; zero past G
+      float x[8] = {};
+      if (half < a.G) load8(sg.q + half * kHeadDim + 8 * l16, x);
+      row_prologue(x, wq, sm.cs, sm.sn, a.rope, a.eps);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= A.scale_log2;
+      for (int e = 0; e < 8; ++e) x[e] = half < a.G ? x[e] * A.scale_log2 : 0.f;
       *reinterpret_cast<float4*>(&qs[half][8 * l16]) = make_float4(x[0], x[1], x[2], x[3]);
       *reinterpret_cast<float4*>(&qs[half][8 * l16 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
     }
-    if (owner && warp == kMathWarps - 1) {
-      float xk[8], xv[8], wk[8];
-      unpack8(uk, xk);
-      unpack8(uv, xv);
-      unpack8(uw, wk);
-      row_prologue(xk, wk, sm.cs, sm.sn, a.rope, a.eps);
-      if (lane == 0) sm.no_page = dst < 0;
+    if (owner && warp == kMathWarps - 1) {                     // both half-warps the same row
+      float x[8], y[8];
+      load8(sg.k + 8 * l16, x);
+      load8(sg.v + 8 * l16, y);
+      row_prologue(x, wk, sm.cs, sm.sn, a.rope, a.eps);
       if (lane < 16) {
-        float rk[8], rv[8];
         if constexpr (kF8) {
-          const uint2 bk = pack_e4m3_row(xk, ks), bv = pack_e4m3_row(xv, vs);
+          const uint2 bk = pack_e4m3_row(x, ks), bv = pack_e4m3_row(y, sg.vs);
           sm.kbits[lane] = make_uint4(bk.x, bk.y, 0, 0);
           sm.vbits[lane] = make_uint4(bv.x, bv.y, 0, 0);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
-            rk[e] = e4m3_to_f32(((e < 4 ? bk.x : bk.y) >> (8 * (e & 3))) & 0xff) * ks;
-            rv[e] = e4m3_to_f32(((e < 4 ? bv.x : bv.y) >> (8 * (e & 3))) & 0xff) * vs;
+            x[e] = e4m3_to_f32(((e < 4 ? bk.x : bk.y) >> (8 * (e & 3))) & 0xff) * ks;
+            y[e] = e4m3_to_f32(((e < 4 ? bv.x : bv.y) >> (8 * (e & 3))) & 0xff) * sg.vs;
           }
         } else {
-          sm.kbits[lane] = pack_bf16_row(xk);
-          sm.vbits[lane] = uv;
-          unpack8(sm.kbits[lane], rk);
-          unpack8(uv, rv);
+          sm.kbits[lane] = pack_bf16_row(x);
+          sm.vbits[lane] = pack_bf16_row(y);
+          unpack8(sm.kbits[lane], x);
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          sm.knew[8 * l16 + e] = rk[e];
-          sm.vnew[8 * l16 + e] = rv[e];
+          sm.knew[8 * l16 + e] = x[e];
+          sm.vnew[8 * l16 + e] = y[e];
         }
       }
     }
     math_sync();
 
     // ---- A operand of S: rows 0-7 the hi parts, rows 8-15 the lo parts of 8 heads.
-    // Over e4m3 a lane's four bytes of a 16-channel chunk are channels 4 tig ..,
+    // Warp kk lays out the fragments of the 16 channels 16 kk .., for all warps.
+    // Over e4m3 a lane's four bytes of such a chunk are channels 4 tig ..,
     // so the chunk's channels are taken in that order by q as well.
-    uint32_t qa[NG][8][4];
 #pragma unroll
-    for (int t = 0; t < NG; ++t)
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const float* q = qs[8 * t + gid] + 16 * kk;
-        const float2 u = *reinterpret_cast<const float2*>(q + (kF8 ? 4 * tig : 2 * tig));
-        const float2 v = *reinterpret_cast<const float2*>(q + (kF8 ? 4 * tig + 2 : 2 * tig + 8));
-        split_pair<kF8>(u.x, u.y, qa[t][kk][0], qa[t][kk][1]);
-        split_pair<kF8>(v.x, v.y, qa[t][kk][2], qa[t][kk][3]);
-      }
+    for (int t = 0; t < NG; ++t) {
+      const float* q = qs[8 * t + gid] + 16 * warp;
+      const float2 u = *reinterpret_cast<const float2*>(q + (kF8 ? 4 * tig : 2 * tig));
+      const float2 v = *reinterpret_cast<const float2*>(q + (kF8 ? 4 * tig + 2 : 2 * tig + 8));
+      uint4 f;
+      split_pair<kF8>(u.x, u.y, f.x, f.y);
+      split_pair<kF8>(v.x, v.y, f.z, f.w);
+      frag[(t * 8 + warp) * 32 + lane] = f;
+    }
     if (owner) {                                               // the new token's scores
       for (int h = warp; h < a.G; h += kMathWarps) {
         const float4 q = *reinterpret_cast<const float4*>(&qs[h][4 * lane]);
-        const float4 k = *reinterpret_cast<const float4*>(&sm.knew[4 * lane]);
-        float z = q.x * k.x + q.y * k.y + q.z * k.z + q.w * k.w;
+        const float4 kn = *reinterpret_cast<const float4*>(&sm.knew[4 * lane]);
+        float z = q.x * kn.x + q.y * kn.y + q.z * kn.z + q.w * kn.w;
 #pragma unroll
         for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
         if (lane == 0) sm.snew[h] = z;
       }
     }
     math_sync();                                               // qs is free for the merge
+    uint4 qf[8];
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) qf[kk] = frag[(t8 + kk) * 32 + lane];
 
     // ---- the segment's keys
     // o: O^T, 8 m-tiles of 16 channels x 8 heads; m (log2 units, less kBias) and
     // l of head gid (a lane's keys only until the end).
-    float o[NG][8][4], m[NG], l[NG];
+    float o[8][4], m = -INFINITY, l = 0.f;
 #pragma unroll
-    for (int t = 0; t < NG; ++t) {
-      m[t] = -INFINITY;
-      l[t] = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
-    }
-    for (int j = 0; j < w.len; ++j, ++n) {
-      if ((n & 1) != (uint32_t)group) continue;
-      const int s = n % C::kStages;
-      if (ok) ok = mbar_wait_warp(smem_u32(&sm.full[s]), (n / C::kStages) & 1, wc);
-      const int pos0 = (w.r.first + w.blk + j) * kBlk + key0;  // the warp's first key
-      if (sm.bad[s]) {
-#pragma unroll
-        for (int t = 0; t < NG; ++t) l[t] = NAN;
-      }
-      if (pos0 < w.r.p && pos0 + 16 > w.r.lo) {
-        const bool edge = pos0 < w.r.lo || pos0 + 16 > w.r.p;
-        const uint32_t kst = ring + s * C::kStageBytes + key_base;
-        const uint32_t vst = kst + kBlk * C::kRowBytes;
+    for (int i = 0; i < 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    const int base = (sg.first + sg.blk) * kBlk + key0;
+    for (int j = (int)((group - n) & (C::kGroups - 1)); j < len; j += C::kGroups) {
+      const uint32_t u = n + j;
+      const int s = u % C::kStages;
+      if (ok) ok = mbar_wait_warp(smem_u32(&sm.full[s]), (u / C::kStages) & 1, wc);
+      const int pos0 = base + j * kBlk;                        // the warp's first key
+      if (sm.bad[s]) l = NAN;
+      if (pos0 < p && pos0 + kKeys > lo) {
+        const bool edge = pos0 < lo || pos0 + kKeys > p;
+        const uint32_t st = ring + s * C::kStageBytes;
         // S of keys pos0 + 8 nt + 2 tig, + 1 for head gid: hi + lo parts
-        float sc[NG][2][2];
+        float sc[4][2];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
-          float acc[NG][2][4];                               // even and odd steps apart
-#pragma unroll
-          for (int t = 0; t < NG; ++t)
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              acc[t][h][0] = acc[t][h][1] = acc[t][h][2] = acc[t][h][3] = 0.f;
-          const int key = nt * 8 + (lane & 7);
+        for (int nt = 0; nt < 4; ++nt) {
+          float acc[2][4] = {};                              // even and odd steps apart
+          const uint32_t kst = st + chunk_at[nt >> 1] + ((nt & 1) * 8 + (lane & 7)) * 128;
           if constexpr (kF8) {
 #pragma unroll
             for (int kq = 0; kq < 2; ++kq) {                 // 64 channels
               uint32_t r[4];
-              ldsm_x4<false>(kst + key * 128 + (((4 * kq + (lane >> 3)) ^ (lane & 7)) << 4), r);
+              ldsm_x4<false>(kst + (((4 * kq + (lane >> 3)) ^ (lane & 7)) << 4), r);
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 uint32_t b0, b1;
                 e4m3x4_to_f16(r[i], b0, b1);
-#pragma unroll
-                for (int t = 0; t < NG; ++t) mma16816<kF8>(acc[t][i & 1], qa[t][4 * kq + i], b0, b1);
+                mma16816<kF8>(acc[i & 1], qf[4 * kq + i], b0, b1);
               }
             }
           } else {
 #pragma unroll
             for (int kp = 0; kp < 4; ++kp) {                 // 32 channels
               uint32_t r[4];
-              ldsm_x4<false>(kst + (kp >> 1) * half_bytes + key * 128 +
+              ldsm_x4<false>(kst + (kp >> 1) * half_bytes +
                                  (((4 * (kp & 1) + (lane >> 3)) ^ (lane & 7)) << 4), r);
 #pragma unroll
               for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int t = 0; t < NG; ++t)
-                  mma16816<kF8>(acc[t][h], qa[t][2 * kp + h], r[2 * h], r[2 * h + 1]);
+                mma16816<kF8>(acc[h], qf[2 * kp + h], r[2 * h], r[2 * h + 1]);
             }
           }
 #pragma unroll
-          for (int t = 0; t < NG; ++t)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              sc[t][nt][e] = (acc[t][0][e] + acc[t][1][e]) + (acc[t][0][2 + e] + acc[t][1][2 + e]);
-              if constexpr (kF8) sc[t][nt][e] *= ks;
-            }
+          for (int e = 0; e < 2; ++e) {
+            sc[nt][e] = (acc[0][e] + acc[1][e]) + (acc[0][2 + e] + acc[1][2 + e]);
+            if constexpr (kF8) sc[nt][e] *= ks;
+          }
         }
-        uint32_t vm0 = 0xffffffffu, vm1 = 0xffffffffu;         // V of keys outside the window: 0
-        if (edge) {
+        uint32_t vm[4] = {0xffffffffu, 0xffffffffu, 0xffffffffu, 0xffffffffu};
+        if (edge) {                                            // V of keys out of view: 0
 #pragma unroll
-          for (int nt = 0; nt < 2; ++nt)
+          for (int nt = 0; nt < 4; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int pos = pos0 + nt * 8 + 2 * tig + e;
-              if (pos < w.r.lo || pos >= w.r.p) {
-#pragma unroll
-                for (int t = 0; t < NG; ++t) sc[t][nt][e] = -INFINITY;
-                (nt ? vm1 : vm0) &= e ? 0x0000ffffu : 0xffff0000u;
+              if (pos < lo || pos >= p) {
+                sc[nt][e] = -INFINITY;
+                vm[nt] &= e ? 0x0000ffffu : 0xffff0000u;
               }
             }
         }
-        uint32_t pb[NG][2];
-#pragma unroll
-        for (int t = 0; t < NG; ++t) {
-          float mx = fmaxf(fmaxf(sc[t][0][0], sc[t][0][1]), fmaxf(sc[t][1][0], sc[t][1][1]));
+        uint32_t pb[4];
+        {
+          float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
+          mx = fmaxf(mx, fmaxf(fmaxf(sc[2][0], sc[2][1]), fmaxf(sc[3][0], sc[3][1])));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
           // lazy: the running max moves only when it grows by more than 2^8
           float alpha = 1.f;
-          if (mx > m[t] + (C::kBias + kRescale)) {
-            alpha = ex2_approx(m[t] - (mx - C::kBias));        // 0 from -inf
-            m[t] = mx - C::kBias;
-            l[t] *= alpha;
+          if (mx > m + (C::kBias + kRescale)) {
+            alpha = ex2_approx(m - (mx - C::kBias));        // 0 from -inf
+            m = mx - C::kBias;
+            l *= alpha;
           }
           if (__any_sync(0xffffffffu, alpha != 1.f)) {
             // this lane's O^T columns are heads 2 tig and 2 tig + 1
@@ -533,98 +669,115 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             const float a1 = __shfl_sync(0xffffffffu, alpha, 8 * tig + 4);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              o[t][i][0] *= a0; o[t][i][1] *= a1; o[t][i][2] *= a0; o[t][i][3] *= a1;
+              o[i][0] *= a0; o[i][1] *= a1; o[i][2] *= a0; o[i][3] *= a1;
             }
           }
-          const float mb = m[t] == -INFINITY ? 0.f : m[t];
-          const float p0 = ex2_approx(sc[t][0][0] - mb), p1 = ex2_approx(sc[t][0][1] - mb);
-          const float p2 = ex2_approx(sc[t][1][0] - mb), p3 = ex2_approx(sc[t][1][1] - mb);
-          l[t] += (p0 + p1) + (p2 + p3);
-          pb[t][0] = kF8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
-          pb[t][1] = kF8 ? pack_f16x2(p2, p3) : pack_bf16x2(p2, p3);
+          const float mb = m == -INFINITY ? 0.f : m;
+          float sum[4];
+#pragma unroll
+          for (int nt = 0; nt < 4; ++nt) {
+            const float p0 = ex2_approx(sc[nt][0] - mb), p1 = ex2_approx(sc[nt][1] - mb);
+            sum[nt] = p0 + p1;
+            pb[nt] = kF8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        if constexpr (kF8) {
-          // ldmatrix on byte pairs: a lane gets channels 2 gid, 2 gid + 1 of keys
-          // 2 tig, 2 tig + 1; rows gid and gid + 8 of the m-tile are those channels
+        const uint32_t vst = st + kBlk * C::kRowBytes;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t r[4], av[2][4];
-            const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
-            ldsm_x4<true>(vst + key * 128 + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4), r);
+        for (int c = 0; c < 2; ++c) {                          // 16 keys
+          if constexpr (kF8) {
+            // ldmatrix on byte pairs: a lane gets channels 2 gid, 2 gid + 1 of keys
+            // 2 tig, 2 tig + 1; rows gid and gid + 8 of the m-tile are those channels
+            const uint32_t row = vst + chunk_at[c] + ((lane & 7) + ((lane >> 3) & 1) * 8) * 128;
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              e4m3x4_to_f16(__byte_perm(r[2 * c], 0, 0x3120), av[c][0], av[c][1]);
-              e4m3x4_to_f16(__byte_perm(r[2 * c + 1], 0, 0x3120), av[c][2], av[c][3]);
-              if (edge) { av[c][0] &= vm0; av[c][1] &= vm0; av[c][2] &= vm1; av[c][3] &= vm1; }
+            for (int i = 0; i < 4; ++i) {
+              uint32_t r[4];
+              ldsm_x4<true>(row + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4), r);
 #pragma unroll
-              for (int t = 0; t < NG; ++t) mma16816<kF8>(o[t][2 * i + c], av[c], pb[t][0], pb[t][1]);
+              for (int d = 0; d < 2; ++d) {
+                uint4 av;
+                e4m3x4_to_f16(__byte_perm(r[2 * d], 0, 0x3120), av.x, av.y);
+                e4m3x4_to_f16(__byte_perm(r[2 * d + 1], 0, 0x3120), av.z, av.w);
+                if (edge) {
+                  av.x &= vm[2 * c]; av.y &= vm[2 * c];
+                  av.z &= vm[2 * c + 1]; av.w &= vm[2 * c + 1];
+                }
+                mma16816<kF8>(o[2 * i + d], av, pb[2 * c], pb[2 * c + 1]);
+              }
             }
-          }
-        } else {
+          } else {
+            const uint32_t row = vst + chunk_at[c] + ((lane & 7) + ((lane >> 4) & 1) * 8) * 128;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t av[4];
-            const int key = (lane & 7) + ((lane >> 4) & 1) * 8;
-            ldsm_x4<true>(vst + (i >> 2) * half_bytes + key * 128 +
-                              (((2 * (i & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), av);
-            if (edge) { av[0] &= vm0; av[1] &= vm0; av[2] &= vm1; av[3] &= vm1; }
-#pragma unroll
-            for (int t = 0; t < NG; ++t) mma16816<kF8>(o[t][i], av, pb[t][0], pb[t][1]);
+            for (int i = 0; i < 8; ++i) {
+              uint32_t r[4];
+              ldsm_x4<true>(row + (i >> 2) * half_bytes +
+                                (((2 * (i & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), r);
+              uint4 av = make_uint4(r[0], r[1], r[2], r[3]);
+              if (edge) {
+                av.x &= vm[2 * c]; av.y &= vm[2 * c];
+                av.z &= vm[2 * c + 1]; av.w &= vm[2 * c + 1];
+              }
+              mma16816<kF8>(o[i], av, pb[2 * c], pb[2 * c + 1]);
+            }
           }
         }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sm.empty[s]));
     }
+    n += len;
 
     // ---- join the warps
     {
-      float* rows = merge + warp * 8 * NG * kMergeRow;
+      float* rows = merge + warp * 8 * kMergeRow;
+      l += __shfl_xor_sync(0xffffffffu, l, 1);
+      l += __shfl_xor_sync(0xffffffffu, l, 2);
+      if (tig == 0) {
+        rows[gid * kMergeRow + kHeadDim] = m;
+        rows[gid * kMergeRow + kHeadDim + 1] = l;
+      }
+      float* r0 = rows + 2 * tig * kMergeRow;
+      float* r1 = r0 + kMergeRow;
 #pragma unroll
-      for (int t = 0; t < NG; ++t) {
-        l[t] += __shfl_xor_sync(0xffffffffu, l[t], 1);
-        l[t] += __shfl_xor_sync(0xffffffffu, l[t], 2);
-        if (tig == 0) {
-          float* r = rows + (8 * t + gid) * kMergeRow;
-          r[kHeadDim] = m[t];
-          r[kHeadDim + 1] = l[t];
-        }
-        float* r0 = rows + (8 * t + 2 * tig) * kMergeRow;
-        float* r1 = r0 + kMergeRow;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int d0 = kF8 ? 16 * i + 2 * gid : 16 * i + gid, d1 = kF8 ? d0 + 1 : d0 + 8;
-          r0[d0] = o[t][i][0];
-          r1[d0] = o[t][i][1];
-          r0[d1] = o[t][i][2];
-          r1[d1] = o[t][i][3];
-        }
+      for (int i = 0; i < 8; ++i) {
+        const int d0 = kF8 ? 16 * i + 2 * gid : 16 * i + gid, d1 = kF8 ? d0 + 1 : d0 + 8;
+        r0[d0] = o[i][0];
+        r1[d0] = o[i][1];
+        r0[d1] = o[i][2];
+        r1[d1] = o[i][3];
       }
     }
     math_sync();                                               // all of the segment's loads seen
-    const bool whole = w.len == w.r.n;
-    const int slot = 2 * blockIdx.x + (w.blk == 0 ? 1 : 0);    // of a partial
-    const bool no_page = owner && sm.no_page;
+    const bool whole = len == sg.n;
+    const int slot = 2 * blockIdx.x + (sg.blk == 0 ? 1 : 0);   // of a partial
+    const bool no_page = owner && sg.dst < 0;
     for (int e = threadIdx.x; e < a.G * (kHeadDim / 4); e += kMathThreads) {
       const int r = e / (kHeadDim / 4), d = 4 * (e % (kHeadDim / 4));
+      // the warps that have head r, as row r % 8 of theirs
+      auto part = [&](int i) {
+        const int wp = NG == 1 ? i : 4 * (i >> 1) + 2 * (r >> 3) + (i & 1);
+        return merge + (wp * 8 + (r & 7)) * kMergeRow;
+      };
       float M = owner ? sm.snew[r] : -INFINITY;
 #pragma unroll
-      for (int i = 0; i < kMathWarps; ++i)
-        M = fmaxf(M, merge[(i * 8 * NG + r) * kMergeRow + kHeadDim]);
-      const float s2 = whole ? __ldg(a.sink + h0 + r) * kLog2e : -INFINITY;
+      for (int i = 0; i < kMathWarps / NG; ++i) M = fmaxf(M, part(i)[kHeadDim]);
+      const float s2 = whole ? sg.sink[r] * kLog2e : -INFINITY;
       M = fmaxf(M, s2);
       const float Mb = M == -INFINITY ? 0.f : M;
       float L = ex2_approx(s2 - Mb);
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int i = 0; i < kMathWarps; ++i) {
-        const float* row = merge + (i * 8 * NG + r) * kMergeRow;
+      for (int i = 0; i < kMathWarps / NG; ++i) {
+        const float* row = part(i);
         const float f = ex2_approx(row[kHeadDim] - Mb);
         const float4 v = *reinterpret_cast<const float4*>(row + d);
         L += row[kHeadDim + 1] * f;
         O.x += v.x * f; O.y += v.y * f; O.z += v.z * f; O.w += v.w * f;
       }
-      O.x *= vs; O.y *= vs; O.z *= vs; O.w *= vs;
+      if constexpr (kF8) {
+        const float vs = sg.vs;
+        O.x *= vs; O.y *= vs; O.z *= vs; O.w *= vs;
+      }
       if (owner) {
         const float f = ex2_approx(sm.snew[r] - Mb);
         const float4 v = *reinterpret_cast<const float4*>(&sm.vnew[d]);
@@ -632,15 +785,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         O.x += v.x * f; O.y += v.y * f; O.z += v.z * f; O.w += v.w * f;
       }
       if (whole) {
-        const long long row = (long long)w.b * a.H + h0 + r;
-        const float inv = 1.f / L;
-        if (a.out_f32)
-          *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kHeadDim + d) =
-              make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-        else
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kHeadDim + d) =
-              make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
-        if (d == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+        write_out(a, (long long)sg.b * a.H + sg.g * a.G + r, d, O, M, L);
       } else {
         *reinterpret_cast<float4*>(A.part_o + ((long long)slot * 16 + r) * kHeadDim + d) = O;
         if (d == 0)
@@ -649,57 +794,77 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
     }
     if (owner && warp == kMathWarps - 1 && lane < 16 && !no_page) {
-      const long long off = dst + w.g * a.c.head_stride;
+      const long long off = sg.dst + sg.g * a.c.head_stride;
       store_bits(a.c, a.c.k, off, sm.kbits[lane]);
       store_bits(a.c, a.c.v, off, sm.vbits[lane]);
     }
     if (no_page && threadIdx.x == 0) atomicOr(a.status, kStatusDecodeRange);
-    if (whole) continue;
-
-    // ---- the last of the pair's segments joins them and adds the sink
-    const long long pair0 = range_begin(units, blockIdx.x, blocks);   // this range's first unit
-    const long long u_seg = pair0 + (range_begin(units, blockIdx.x + 1, blocks) - pair0) - w.left;
-    const long long u_pair = u_seg - w.blk;
-    const int c0 = range_of(units, u_pair, blocks), c1 = range_of(units, u_pair + w.r.n - 1, blocks);
-    __threadfence();
-    math_sync();
-    if (threadIdx.x == 0) {
-      int* counter = A.counters + (long long)w.b * a.c.Hk + w.g;
-      const int done = atomicAdd(counter, 1) == c1 - c0;
-      if (done) *counter = 0;                                  // ready for the next call
-      sm.last = done;
+    if (!whole) {                                              // to be joined at the end
+      const Part q{sg.b, sg.g, sg.c0, sg.c1};
+      if (sg.blk == 0) last_part = q;
+      else first_part = q;
     }
-    math_sync();
-    if (!sm.last) continue;
-    __threadfence();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[k % kSegs]));
+  }
+
+  // ---- the last of a pair's segments to finish joins them and adds the sink.
+  // Both of a block's partials (its range's first and last segment) are counted
+  // here, after all of its loads, so that no join holds up the stream.
+  if (first_part.b < 0 && last_part.b < 0) return;
+  math_sync();                                                 // the partials are written
+  if (threadIdx.x % (kMathThreads / 2) == 0) {                 // one thread for each partial
+    const int i = threadIdx.x / (kMathThreads / 2);
+    const Part q = i ? last_part : first_part;
+    int last = 0;
+    if (q.b >= 0) {
+      __threadfence();
+      int* counter = A.counters + (long long)q.b * a.c.Hk + q.g;
+      if (atomicAdd(counter, 1) == q.c1 - q.c0) {
+        __threadfence();
+        *counter = 0;                                          // ready for the next call
+        last = 1;
+      }
+    }
+    sm.last[i] = last;
+  }
+  math_sync();
+#pragma unroll 1
+  for (int i = 0; i < 2; ++i) {
+    if (!sm.last[i]) continue;
+    const Part q = i ? last_part : first_part;
+    const int h0 = q.g * a.G;
     for (int e = threadIdx.x; e < a.G * (kHeadDim / 4); e += kMathThreads) {
       const int r = e / (kHeadDim / 4), d = 4 * (e % (kHeadDim / 4));
-      const float s2 = __ldg(a.sink + h0 + r) * kLog2e;
-      float M = s2;
-#pragma unroll 8
-      for (int c = c0; c <= c1; ++c)
-        M = fmaxf(M, __ldcg(A.part_ml + ((2LL * c + (c == c0)) * 16 + r) * 2));
-      const float Mb = M == -INFINITY ? 0.f : M;
-      float L = ex2_approx(s2 - Mb);
+      // in the order of the ranges, whoever joins; the sink first
+      float M = __ldg(a.sink + h0 + r) * kLog2e, L = 1.f;
       float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (int c = c0; c <= c1; ++c) {
-        const long long at = (2LL * c + (c == c0)) * 16 + r;
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(A.part_ml) + at);
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(A.part_o + at * kHeadDim + d));
-        const float f = ex2_approx(ml.x - Mb);
-        L += ml.y * f;
-        O.x += v.x * f; O.y += v.y * f; O.z += v.z * f; O.w += v.w * f;
+      constexpr int kAtOnce = 8;                               // partials in flight
+      for (int c = q.c0; c <= q.c1; c += kAtOnce) {
+        float2 ml[kAtOnce];
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const int cu = c + u;
+          const long long at = (2LL * cu + (cu == q.c0)) * 16 + r;
+          ml[u] = make_float2(-INFINITY, 0.f);
+          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (cu <= q.c1) {
+            ml[u] = __ldcg(reinterpret_cast<const float2*>(A.part_ml) + at);
+            v[u] = __ldcg(reinterpret_cast<const float4*>(A.part_o + at * kHeadDim + d));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) {
+          const float mn = fmaxf(M, ml[u].x), mb = mn == -INFINITY ? 0.f : mn;
+          const float f = ex2_approx(M - mb), t = ex2_approx(ml[u].x - mb);
+          M = mn;
+          L = L * f + ml[u].y * t;
+          O.x = O.x * f + v[u].x * t; O.y = O.y * f + v[u].y * t;
+          O.z = O.z * f + v[u].z * t; O.w = O.w * f + v[u].w * t;
+        }
       }
-      const long long row = (long long)w.b * a.H + h0 + r;
-      const float inv = 1.f / L;
-      if (a.out_f32)
-        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kHeadDim + d) =
-            make_float4(O.x * inv, O.y * inv, O.z * inv, O.w * inv);
-      else
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * kHeadDim + d) =
-            make_uint2(pack_bf16x2(O.x * inv, O.y * inv), pack_bf16x2(O.z * inv, O.w * inv));
-      if (d == 0) a.lse[row] = (M + log2f(L)) * kLn2;
+      write_out(a, (long long)q.b * a.H + h0 + r, d, O, M, L);
     }
   }
 }
@@ -710,7 +875,7 @@ template <int NG, bool kF8>
 cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Args& A, int grid,
                    cudaStream_t st) {
   static PerDeviceOnce once;
-  constexpr int bytes = smem_bytes<NG, kF8>();
+  constexpr int bytes = Cfg<NG, kF8>::kSmemBytes;
   static_assert(bytes <= 227 * 1024, "exceeds the shared memory of one block");
   cudaError_t e = smem_limit_once(once, decode_paged_kernel<NG, kF8>, bytes);
   if (e != cudaSuccess) return e;

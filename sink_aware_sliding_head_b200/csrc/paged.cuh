@@ -8,6 +8,7 @@
 // (strides in elements), so head-major [pages, Hk, P, D] and token-major
 // [pages, P, Hk, D] pools, or K and V interleaved in one tensor, are one case.
 #pragma once
+#include <cmath>
 #include <cuda.h>
 #include <cuda_fp8.h>
 
@@ -36,14 +37,29 @@ __device__ __forceinline__ long long slot_offset(const PagedCache& c, int b, int
   return page * c.page_stride + (pos - col * c.P) * c.token_stride;
 }
 
-// cos and sin of pos * theta^(-2j/D). The angle is formed and reduced in
-// double: at position 131071 a float angle would be off by 0.004 rad.
-__device__ __forceinline__ void rope_cos_sin(int pos, int j, double log2_theta, float* c,
+// RoPE's frequencies in turns a position, theta^(-2j/D) / 2 pi for j < 64, as
+// powers: pow[i] = theta^(-2^i / 64), so six products in double give any of them.
+struct RopePowers {
+  double pow[6];
+};
+inline RopePowers rope_powers(double theta) {
+  RopePowers r;
+  for (int i = 0; i < 6; ++i) r.pow[i] = std::exp2(-(double)(1 << i) / 64 * std::log2(theta));
+  return r;
+}
+// cos and sin of pos * theta^(-2j/D). The angle is formed and reduced in double:
+// in float it would be off by 0.004 rad at position 131071. Taking it in turns
+// makes the reduction exact and lets sinpi / cospi do without their own (with
+// exp2 and sincosf here, a table of 64 angles took 5000 cycles).
+__device__ __forceinline__ void rope_cos_sin(int pos, int j, const RopePowers& w, float* c,
                                              float* s) {
-  const double inv_2pi = 0.15915494309189533577, two_pi = 6.283185307179586476925;
-  double a = (double)pos * exp2(-(2.0 / kHeadDim) * j * log2_theta);
-  a -= two_pi * rint(a * inv_2pi);
-  sincosf((float)a, s, c);
+  double f = 0.15915494309189533577;         // 1 / 2 pi
+#pragma unroll
+  for (int i = 0; i < 6; ++i)
+    if (j & (1 << i)) f *= w.pow[i];
+  double turns = (double)pos * f;
+  turns -= rint(turns);
+  sincospif(2.f * (float)turns, s, c);
 }
 
 __device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
@@ -128,7 +144,7 @@ struct PagedAppendLaunch {
   PagedCache c;
   int N, T, rope;
   long long k_stride, v_stride;   // elements between tokens
-  double log2_theta;
+  RopePowers rope_pow;
   float eps;
   const __nv_bfloat16 *k, *v, *wk;
   const int32_t *cu, *lens;
@@ -140,7 +156,7 @@ struct PagedDecodeLaunch {
   PagedCache c;
   int B, H, G, W, rope, out_f32;
   long long q_stride, k_stride, v_stride;
-  double log2_theta;
+  RopePowers rope_pow;
   float eps, scale;
   const __nv_bfloat16 *q, *k, *v, *wq, *wk;
   const float* sink;

@@ -47,7 +47,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedAppen
   if (a.rope) {
     for (int e = threadIdx.x; e < kTok * (kHeadDim / 2); e += kThreads) {
       const int i = e / (kHeadDim / 2), j = e % (kHeadDim / 2);
-      rope_cos_sin(pos_s[i], j, a.log2_theta, &cs[i][j], &sn[i][j]);
+      rope_cos_sin(pos_s[i], j, a.rope_pow, &cs[i][j], &sn[i][j]);
     }
     __syncthreads();
   }

@@ -1,12 +1,13 @@
 """The load ring of the paged decode kernel, restated and run on the CPU.
 
-One warp streams blocks of keys through S shared-memory stages; two groups of four warps take
-the blocks in turn (block n: stage n % S, group n % 2). A stage has a "full" barrier (the
-loading warp arrives, and the copies complete their bytes) and an "empty" one (the four warps
-arrive). Copies land in any order. mbarrier waits test a phase's parity only, so a wait that
-is two phases behind passes at once: with an odd S a stage changes hands between the groups,
-a group does not see every phase of it, and a copy that lands late lets the other group read
-a stage before its own copy is there. With an even S each stage belongs to one group.
+Blocks of keys stream through S shared-memory stages; four groups of two math warps (two of
+four over more than 8 heads) take the blocks in turn (block n: stage n % S, group n % 4). A stage has a "full" barrier (the
+loading warp arrives, and the copies complete their bytes) and an "empty" one (the group's
+warps arrive). Copies land in any order. mbarrier waits test a phase's parity only, so a wait
+that is two phases behind passes at once: when S is no multiple of the groups, a stage changes
+hands between them, a group does not see every phase of it, and a copy that lands late lets
+another group read a stage before its own copy is there. Otherwise each stage belongs to one
+group.
 """
 import random
 import re
@@ -15,7 +16,7 @@ import pytest
 
 from sink_aware_sliding_head_b200.build import CSRC
 
-GROUP_WARPS = 4
+GROUPS, GROUP_WARPS = 4, 2
 
 
 class Barrier:
@@ -52,7 +53,7 @@ def run(stages, units, seed):
     empty = [Barrier(GROUP_WARPS) for _ in range(stages)]
     holds = [None] * stages                       # the block whose bytes are in the stage
     flying, issued = [], 0
-    warps = [(g, w) for g in (0, 1) for w in range(GROUP_WARPS)]
+    warps = [(g, w) for g in range(GROUPS) for w in range(GROUP_WARPS)]
     at = {x: x[0] for x in warps}
     slow = rng.random()
     for _ in range(400 * units + 4000):
@@ -76,30 +77,31 @@ def run(stages, units, seed):
                 if holds[n % stages] != n:
                     return False
                 empty[n % stages].arrive()
-                at[x] = n + 2
+                at[x] = n + GROUPS
     return False
 
 
-def test_even_rings_keep_their_order():
-    for stages in (2, 4, 6, 8, 10):
+def test_rings_of_whole_turns_keep_their_order():
+    for stages in (4, 8, 12):
         for seed in range(60):
             assert run(stages, 5 * stages + seed % 7, seed), (stages, seed)
 
 
-def test_an_odd_ring_is_caught():
+@pytest.mark.parametrize("stages", [5, 6])
+def test_other_rings_are_caught(stages):
     def ends_badly(seed):
         try:
-            return not run(5, 40, seed)
+            return not run(stages, 40, seed)
         except AssertionError:
             return True
     assert any(ends_badly(seed) for seed in range(60))
 
 
-def test_the_kernel_uses_even_rings():
+def test_the_kernel_uses_such_rings():
     src = open(f"{CSRC}/decode_paged.cu").read()
-    m = re.search(r"kStages = \(NG == 1 \? (\d+) : (\d+)\) \* \(kF8 \? (\d+) : 1\)", src)
+    m = re.search(r"kStages = kF8 \? (\d+) : (\d+);", src)
     assert m, "the ring sizes moved: adapt this test"
-    one, two, f8 = map(int, m.groups())
-    for s in (one, two, one * f8, two * f8):
-        assert s % 2 == 0 and s <= 16
-    assert "static_assert(kStages % 2 == 0" in src
+    assert all(int(s) % GROUPS == 0 for s in m.groups())
+    assert "static_assert(kStages % kGroups == 0" in src
+    assert "kGroupWarps = 2 * NG, kGroups = kMathWarps / kGroupWarps" in src
+    assert "constexpr int kMathWarps = 8;" in src and "constexpr int kLoadWarps = 4;" in src
