@@ -64,10 +64,11 @@ struct __align__(16) Seg {
   __nv_bfloat16 q[16 * kHeadDim], k[kHeadDim], v[kHeadDim];    // raw rows (k, v: last segment)
   float sink[16], ks, vs;
   long long dst;                             // the new token's slot (KV head 0), -1: no page
-  int b, g;                                  // b = -1: no more segments
+  int b, g;
   int blk, len, n;                           // blocks blk .. blk + len - 1 of the pair's n
   int p, lo, first;                          // of the row, as in Range
   int c0, c1;                                // the ranges that share the pair
+  int final;                                 // the range's last segment
 };
 struct Small {
   uint64_t full[16], empty[16], seg_full[kSegs], seg_empty[kSegs];
@@ -108,6 +109,7 @@ struct Cfg {
 struct Args {
   PagedDecodeLaunch a;
   int box;                                   // slots per TMA box: 16, 32 or 64
+  uint32_t page_mul, page_shift;             // pos / P = umulhi(pos, page_mul) >> page_shift
   float scale_log2;
   int* counters;                             // [B * Hk], zero between calls
   float* part_ml;                            // [2 * blocks][16][2]
@@ -129,16 +131,9 @@ __device__ __forceinline__ Range row_range(const PagedDecodeLaunch& a, int p) {
     r.n = p > r.lo ? (p - 1) / kBlk - r.first + 1 : 1;   // 1: only the new token
   return r;
 }
-// First unit of block i's range, and the block whose range holds unit u.
 // (Quotients of numbers below 2^32 take the short division.)
 __device__ __forceinline__ long long quotient(long long x, long long y) {
   return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
-}
-__device__ __forceinline__ long long range_begin(long long units, int i, int blocks) {
-  return quotient(units * i, blocks);
-}
-__device__ __forceinline__ int range_of(long long units, long long u, int blocks) {
-  return (int)quotient((u + 1) * blocks - 1, units);
 }
 
 // The segments of one block's range, in order.
@@ -169,6 +164,9 @@ struct Walk {
 };
 
 // ------------------------------------------------------------------ small pieces
+__device__ __forceinline__ int page_col(const Args& A, int pos) {
+  return (int)(__umulhi((uint32_t)pos, A.page_mul) >> A.page_shift);
+}
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, uint32_t bar,
                                             int slot, int head, int page) {
   asm volatile(
@@ -289,8 +287,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 
   // ---- the plan: all units, and where this block's range begins
-  long long units, left;
-  int blocks;                                // that have a range: no range is empty
+  long long share, u0, left;                 // units a range; this one's first and count
   {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
@@ -316,11 +313,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (i < warp) before += sm.scan[i];
       total += sm.scan[i];
     }
-    units = total * a.c.Hk;
-    blocks = (int)min((long long)gridDim.x, units);
-    if ((int)blockIdx.x >= blocks) return;
-    const long long u0 = range_begin(units, blockIdx.x, blocks);
-    left = range_begin(units, blockIdx.x + 1, blocks) - u0;
+    // At least a block for each group of math warps: those take as long as one
+    // (230 keys, 4 KV heads: 9.5 us in four ranges a pair and a join, 6.9 in one).
+    const long long units = total * a.c.Hk;
+    share = max(quotient(units + gridDim.x - 1, gridDim.x), (long long)C::kGroups);
+    u0 = share * blockIdx.x;
+    left = units - u0 < share ? units - u0 : share;
+    if (left <= 0) return;
     long long at = u0 - before * a.c.Hk;
     if (at >= 0 && at < sum * a.c.Hk) {
       int b = b0;
@@ -347,6 +346,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int nbox = kBlk / A.box;                             // 1, 2 or 4 boxes a block
     const uint32_t box_bytes = (uint32_t)A.box * C::kRowBytes;
     const uint32_t lw = warp - kMathWarps;                     // takes blocks n % 4 == lw
+    const bool describes = lw == kLoadWarps - 1;               // not the one with block 0
     uint32_t n = 0, k = 0, issued = 0;                         // issued: its last block + 1
     bool ok = true;
     Walk w;
@@ -362,66 +362,77 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     auto fetch = [&](const Walk& v, int at) {
       const int i = at + lane, pos = (v.r.first + v.blk) * kBlk + i * A.box;
       const bool need = i < v.len * nbox && pos + A.box > v.r.lo && pos < v.r.p;
-      const int col = pos / a.c.P;
+      const int col = page_col(A, pos);
       const int32_t* row = a.c.table + v.b * a.c.table_stride;
       return Box{need ? max(__ldg(row + col), -1) : -2, pos - col * a.c.P};
     };
     // What a segment needs besides keys, requested one segment ahead.
-    struct Ahead { Box box; long long dst; float sink, ks, vs; };
+    struct Ahead { Box box; int page, slot; float sink, ks, vs; };
     auto look = [&](const Walk& v) {
       Ahead h;
       h.box = fetch(v, 0);
-      h.dst = slot_offset(a.c, v.b, v.r.p);
-      h.sink = lane < a.G ? __ldg(a.sink + v.g * a.G + lane) : 0.f;
-      h.ks = kF8 && a.c.k_scale ? __ldg(a.c.k_scale + v.g) : 1.f;
-      h.vs = kF8 && a.c.v_scale ? __ldg(a.c.v_scale + v.g) : 1.f;
+      if (describes) {
+        const int col = page_col(A, v.r.p);
+        h.page = __ldg(a.c.table + v.b * a.c.table_stride + col);
+        h.slot = v.r.p - col * a.c.P;
+        h.sink = lane < a.G ? __ldg(a.sink + v.g * a.G + lane) : 0.f;
+        h.ks = kF8 && a.c.k_scale ? __ldg(a.c.k_scale + v.g) : 1.f;
+        h.vs = kF8 && a.c.v_scale ? __ldg(a.c.v_scale + v.g) : 1.f;
+      }
       return h;
     };
     Ahead h = look(w);
     while (true) {
       // ---- describe the segment
-      Seg& sg = segs[k % kSegs];
-      if (lw == 0 && k >= kSegs)
-        ok = mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc);
-      if (!ok) break;
-      const bool owner = w.blk + w.len == w.r.n;
-      if (lw == 0 && lane < 16) sg.sink[lane] = h.sink;
-      if (lw == 0 && lane == 0) {
-        sg.ks = h.ks;
-        sg.vs = h.vs;
-        sg.dst = h.dst;
-        sg.b = w.b;
-        sg.g = w.g;
-        sg.blk = w.blk;
-        sg.len = w.len;
-        sg.n = w.r.n;
-        sg.p = w.r.p;
-        sg.lo = w.r.lo;
-        sg.first = w.r.first;
-        if (w.len < w.r.n) {
-          const long long u_pair = range_begin(units, blockIdx.x + 1, blocks) - w.left - w.blk;
-          sg.c0 = range_of(units, u_pair, blocks);
-          sg.c1 = range_of(units, u_pair + w.r.n - 1, blocks);
-        }
-      }
-      __syncwarp();
-      if (lw == 0 && lane == 0) {
+      if (describes) {
+        Seg& sg = segs[k % kSegs];
+        if (k >= kSegs)
+          ok = mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc);
+        if (!ok) break;
+        const bool owner = w.blk + w.len == w.r.n;
         const uint32_t bar = smem_u32(&sm.seg_full[k % kSegs]);
         const uint32_t q_bytes = (uint32_t)a.G * kHeadDim * 2, row = kHeadDim * 2;
-        mbar_arrive_expect_tx(bar, q_bytes + (owner ? 2 * row : 0));
-        bulk_load(smem_u32(sg.q), a.q + w.b * a.q_stride + (long long)w.g * a.G * kHeadDim,
-                  q_bytes, bar);
-        if (owner) {
-          bulk_load(smem_u32(sg.k), a.k + w.b * a.k_stride + w.g * kHeadDim, row, bar);
-          bulk_load(smem_u32(sg.v), a.v + w.b * a.v_stride + w.g * kHeadDim, row, bar);
+        if (lane == 0) {                                       // their bytes may land before
+          bulk_load(smem_u32(sg.q), a.q + w.b * a.q_stride + (long long)w.g * a.G * kHeadDim,
+                    q_bytes, bar);                             // the barrier expects them
+          if (owner) {
+            bulk_load(smem_u32(sg.k), a.k + w.b * a.k_stride + w.g * kHeadDim, row, bar);
+            bulk_load(smem_u32(sg.v), a.v + w.b * a.v_stride + w.g * kHeadDim, row, bar);
+          }
+          sg.b = w.b;
+          sg.g = w.g;
+          sg.blk = w.blk;
+          sg.len = w.len;
+          sg.n = w.r.n;
+          sg.p = w.r.p;
+          sg.lo = w.r.lo;
+          sg.first = w.r.first;
+          sg.final = w.left == w.len;
+          if (w.len < w.r.n) {
+            const long long u_pair = u0 + left - w.left - w.blk;
+            sg.c0 = (int)quotient(u_pair, share);
+            sg.c1 = (int)quotient(u_pair + w.r.n - 1, share);
+          }
+          sg.ks = h.ks;
+          sg.vs = h.vs;
+          sg.dst = (unsigned)h.page < (unsigned)a.c.num_pages
+                       ? h.page * a.c.page_stride + h.slot * a.c.token_stride : -1;
         }
+        if (lane < 16) sg.sink[lane] = h.sink;
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(bar, q_bytes + (owner ? 2 * row : 0));
       }
       ++k;
       // ---- its keys
       Walk nx = w;
-      const bool more = nx.next(a, sm.lens);
-      Box cur = h.box, ahead = fetch(w, 32);
-      if (more) h = look(nx);
+      Box cur = h.box, ahead{};
+      bool more = false, looked = false;
+      auto look_ahead = [&] {                                  // after the first block's copies
+        ahead = fetch(w, 32);
+        more = nx.next(a, sm.lens);
+        if (more) h = look(nx);
+        looked = true;
+      };
       int batch = 0;
       for (int j = (int)((lw - n) & (kLoadWarps - 1)); j < w.len; j += kLoadWarps) {
         const int i = j * nbox;                                // the block's first box
@@ -454,19 +465,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           tma_load_5d(dst + kBlk * C::kRowBytes, &tm_v, full, slot, w.g, page);
         }
         __syncwarp();
+        if (!looked) look_ahead();
       }
+      if (!looked) look_ahead();
       n += w.len;
       if (!ok || !more) break;
       w = nx;
-    }
-    const uint32_t described = k;
-    if (ok && lw == 0) {                                                  // the end
-      if (k >= kSegs)
-        ok = mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc);
-      if (ok && lane == 0) {
-        segs[k % kSegs].b = -1;
-        mbar_arrive(smem_u32(&sm.seg_full[k % kSegs]));
-      }
     }
     // Every copy has landed before the block can exit (immediate unless a wait
     // ran out: the math warps saw each one).
@@ -475,8 +479,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     for (uint32_t u = issued > C::kStages ? issued - C::kStages : 0; u < issued; ++u)
       if (u % kLoadWarps == lw)
         mbar_wait_warp(smem_u32(&sm.full[u % C::kStages]), (u / C::kStages) & 1, drain);
-    for (uint32_t i = described > kSegs ? described - kSegs : 0; i < described; ++i)
-      if (lw == 0 && (i + kSegs > k || !ok))                   // not yet described anew
+    if (describes && ok)                                       // (a failed wait described none)
+      for (uint32_t i = k > kSegs ? k - kSegs : 0; i < k; ++i)
         mbar_wait_warp(smem_u32(&sm.seg_full[i % kSegs]), (i / kSegs) & 1, drain);
     return;
   }
@@ -505,13 +509,17 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   // earlier range (first), and of one that goes on in a later range (last).
   struct Part { int b, g, c0, c1; } first_part{-1, 0, 0, 0}, last_part{-1, 0, 0, 0};
 
+  if (a.rope && threadIdx.x < kHeadDim / 2) {                  // while the first rows come
+    last_b = sm.start_b;
+    rope_cos_sin(sm.lens[a.B > kLensKept ? 0 : last_b], threadIdx.x, a.rope_pow,
+                 &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
+  }
   for (uint32_t k = 0;; ++k) {
     const Seg& sg = segs[k % kSegs];
     if (ok) ok = mbar_wait_warp(smem_u32(&sm.seg_full[k % kSegs]), (k / kSegs) & 1, wc);
-    if (ok && a.rope && sg.b >= 0 && sg.b != last_b && threadIdx.x < kHeadDim / 2)
+    if (ok && a.rope && sg.b != last_b && threadIdx.x < kHeadDim / 2)
       rope_cos_sin(sg.p, threadIdx.x, a.rope_pow, &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
     if (!math_sync_and(ok)) break;                             // table; merge area free
-    if (sg.b < 0) break;
     last_b = sg.b;
     const int len = sg.len, p = sg.p, lo = sg.lo;
     const bool owner = sg.blk + len == sg.n;                   // this segment has the new token
@@ -804,7 +812,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (sg.blk == 0) last_part = q;
       else first_part = q;
     }
+    const bool final = sg.final;
     __syncwarp();
+    if (final) break;
     if (lane == 0) mbar_arrive(smem_u32(&sm.seg_empty[k % kSegs]));
   }
 
@@ -898,6 +908,11 @@ cudaError_t launch_decode_paged(const PagedDecodeLaunch& a, int num_sms, cudaStr
   Args A;
   A.a = a;
   A.box = a.c.P % 64 == 0 ? 64 : a.c.P % 32 == 0 ? 32 : 16;
+  // ceil(2^(31 + s) / P) with 2^s >= P gives exact quotients of numbers below 2^31
+  uint32_t s = 0;
+  while ((1u << s) < (uint32_t)a.c.P) ++s;
+  A.page_mul = (uint32_t)(((1ull << (31 + s)) + a.c.P - 1) / a.c.P);
+  A.page_shift = s - 1;
   A.scale_log2 = a.scale * kLog2e;
   uint8_t* ws = reinterpret_cast<uint8_t*>(a.status);
   const size_t rows = (size_t)2 * num_sms * 16;
