@@ -10,7 +10,8 @@
 // the G query heads of its group, 2 G operations a byte.
 //
 //   * Work. The keys of all (sequence, KV head) pairs are laid end to end in
-//     blocks of 64 positions and cut into one equal range per SM. A block of
+//     blocks of 64 positions, each pair behind a few units of nothing that stand
+//     for its fixed cost, and cut into one equal range per SM. A block of
 //     threads walks its range as segments of one pair each; a segment that is a
 //     whole pair writes its result, the others leave an unnormalised partial
 //     (m, l, O) and the last of a pair's segments to finish joins them. The plan
@@ -91,6 +92,10 @@ struct Cfg {
   // A multiple of the groups: the groups take the blocks in turn, so each stage
   // then belongs to one group, which sees every phase of its barriers. In any
   // other ring a group's parity wait could be two phases behind and pass early.
+  // A pair's fixed cost in units. 201 rows of up to 2513 keys, nine heads to a KV
+  // head, cost 0, 4, 8, 12: 54.1, 43.8, 44.8, - us in bf16, 58.4, 45.8, 44.9, 46.3
+  // in e4m3; 250 rows of up to 900: 71.8, 53.2, 54.2, - and 76.0, 53.1, 47.5, 47.3.
+  static constexpr int kCost = kF8 ? 8 : 4;
   static constexpr int kGroupWarps = 2 * NG, kGroups = kMathWarps / kGroupWarps;
   static constexpr int kStages = kF8 ? 8 : 4;
   static_assert(kStages % kGroups == 0 && kStages <= 16, "see above");
@@ -136,31 +141,39 @@ __device__ __forceinline__ long long quotient(long long x, long long y) {
   return ((x | y) >> 32) == 0 ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
 }
 
-// The segments of one block's range, in order.
+// The segments of one block's range, in order. A pair of n blocks is cost + n
+// units; a segment is the blocks among a range's units of one pair.
 struct Walk {
+  int cost;
   int b, b0;                                 // row; the first whose lens is kept
-  long long off, left;                       // unit within the row's n * Hk; units left
+  long long off, left;                       // unit within the row's (cost + n) * Hk; units left
   Range r;
   int g, blk, len;                           // the segment: KV head, blocks of the pair's r.n
-  __device__ void cut() {
-    g = (int)quotient(off, r.n);
-    blk = (int)(off - (long long)g * r.n);
-    len = (int)min((long long)(r.n - blk), left);
+  int units;                                 // of the pair in this range
+  // false: nothing but a pair's fixed cost is left
+  __device__ bool cut() {
+    g = (int)quotient(off, cost + r.n);
+    const int at = (int)(off - (long long)g * (cost + r.n));
+    units = (int)min((long long)(cost + r.n - at), left);
+    blk = max(0, at - cost);
+    len = max(0, at + units - cost) - blk;
+    return len > 0;
   }
   __device__ bool next(const PagedDecodeLaunch& a, const int* lens) {
-    off += len;
-    left -= len;
-    if (left == 0) return false;
-    if (off == (long long)r.n * a.c.Hk) {
+    off += units;
+    left -= units;
+    if (left <= 0) return false;
+    if (off == (long long)(cost + r.n) * a.c.Hk) {
       off = 0;
       do {                                   // ends: left > 0 units lie in later rows
         ++b;
         r = row_range(a, b - b0 < kLensKept ? lens[b - b0] : __ldg(a.lens + b));
       } while (r.n == 0);
     }
-    cut();
-    return true;
+    return cut();
   }
+  // Whether this is the range's last segment: what may follow is less than a block.
+  __device__ bool final() const { return left - units <= cost; }
 };
 
 // ------------------------------------------------------------------ small pieces
@@ -287,8 +300,37 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   }
 
   // ---- the plan: all units, and where this block's range begins
-  long long share, u0, left;                 // units a range; this one's first and count
-  {
+  Walk w;
+  long long share, u0;                       // units a range; this one's first
+  if (a.B == 1) {
+    // One row's pairs are all alike: each gets ranges of its own, as many as
+    // there are SMs for, but not below a block for each group of math warps
+    // (those take as long as one: 230 keys took 9.5 us in four ranges a pair and
+    // a join, 7.2 in one); the cost fills up a pair's last range.
+    w.b = w.b0 = 0;
+    w.r = row_range(a, __ldg(a.lens));
+    __syncthreads();
+    const int n = w.r.n, most = (int)gridDim.x / a.c.Hk;
+    if (n == 0) {
+      if (w.r.p != -1 && blockIdx.x == 0 && threadIdx.x == 0)
+        atomicOr(a.status, kStatusDecodeRange);
+      return;
+    }
+    if (most > 0) {
+      const int ranges = min(most, (n + C::kGroups - 1) / C::kGroups);
+      share = (n + ranges - 1) / ranges;
+      w.cost = (int)((n + share - 1) / share * share - n);
+    } else {                                 // more KV heads than SMs: several pairs a range
+      w.cost = C::kCost;
+      share = (long long)(w.cost + n) * ((a.c.Hk + gridDim.x - 1) / gridDim.x);
+    }
+    const long long units = (long long)(w.cost + n) * a.c.Hk;
+    u0 = share * blockIdx.x;
+    w.off = u0;
+    w.left = units - u0 < share ? units - u0 : share;
+    if (w.left <= 0) return;
+  } else {
+    w.cost = C::kCost;
     const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
     long long sum = 0;
@@ -296,7 +338,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int p = __ldg(a.lens + b);
       const Range r = row_range(a, p);
       if (a.B <= kLensKept) sm.lens[b] = p;
-      sum += r.n;
+      sum += r.n ? w.cost + r.n : 0;
       if (r.n == 0 && r.p != -1 && blockIdx.x == 0) atomicOr(a.status, kStatusDecodeRange);
     }
     long long incl = sum;
@@ -313,21 +355,19 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (i < warp) before += sm.scan[i];
       total += sm.scan[i];
     }
-    // At least a block for each group of math warps: those take as long as one
-    // (230 keys, 4 KV heads: 9.5 us in four ranges a pair and a join, 6.9 in one).
     const long long units = total * a.c.Hk;
-    share = max(quotient(units + gridDim.x - 1, gridDim.x), (long long)C::kGroups);
+    share = max(quotient(units + gridDim.x - 1, gridDim.x), (long long)(w.cost + C::kGroups));
     u0 = share * blockIdx.x;
-    left = units - u0 < share ? units - u0 : share;
-    if (left <= 0) return;
+    w.left = units - u0 < share ? units - u0 : share;
+    if (w.left <= 0) return;
     long long at = u0 - before * a.c.Hk;
     if (at >= 0 && at < sum * a.c.Hk) {
       int b = b0;
       for (;; ++b) {                         // ends inside b0 .. b1-1: at < sum * Hk
-        const int p = a.B <= kLensKept ? sm.lens[b] : __ldg(a.lens + b);
-        const long long n = (long long)row_range(a, p).n * a.c.Hk;
-        if (at < n) break;
-        at -= n;
+        const int n = row_range(a, a.B <= kLensKept ? sm.lens[b] : __ldg(a.lens + b)).n;
+        const long long units_b = n ? (long long)(w.cost + n) * a.c.Hk : 0;
+        if (at < units_b) break;
+        at -= units_b;
       }
       sm.start_b = b;
       sm.start_off = at;
@@ -338,7 +378,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         sm.lens[i] = __ldg(a.lens + sm.start_b + i);
       __syncthreads();
     }
+    w.b = sm.start_b;
+    w.b0 = a.B > kLensKept ? w.b : 0;
+    w.off = sm.start_off;
+    w.r = row_range(a, sm.lens[w.b - w.b0]);
   }
+  const long long u_end = u0 + w.left;
+  if (!w.cut()) return;                      // not a block in this range
   const WaitCtx wc{&sm.abort_flag, a.status, kStatusTimeoutFwd};
 
   if (warp >= kMathWarps) {
@@ -349,13 +395,6 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const bool describes = lw == kLoadWarps - 1;               // not the one with block 0
     uint32_t n = 0, k = 0, issued = 0;                         // issued: its last block + 1
     bool ok = true;
-    Walk w;
-    w.b = sm.start_b;
-    w.b0 = a.B > kLensKept ? w.b : 0;
-    w.off = sm.start_off;
-    w.left = left;
-    w.r = row_range(a, sm.lens[w.b - w.b0]);
-    w.cut();
     // The table is read 32 boxes at a time and ahead: lane i holds the page and
     // slot of box at + i of a segment (-2: nothing visible; -1: a bad page).
     struct Box { int page, slot; };
@@ -407,11 +446,13 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           sg.p = w.r.p;
           sg.lo = w.r.lo;
           sg.first = w.r.first;
-          sg.final = w.left == w.len;
+          sg.final = w.final();
           if (w.len < w.r.n) {
-            const long long u_pair = u0 + left - w.left - w.blk;
-            sg.c0 = (int)quotient(u_pair, share);
-            sg.c1 = (int)quotient(u_pair + w.r.n - 1, share);
+            // the pair's first and last block are units of these ranges
+            const long long end = u_end - w.left + w.units;
+            const long long last = end - 1 + (w.r.n - w.blk - w.len);
+            sg.c0 = (int)quotient(last - (w.r.n - 1), share);
+            sg.c1 = (int)quotient(last, share);
           }
           sg.ks = h.ks;
           sg.vs = h.vs;
@@ -510,9 +551,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   struct Part { int b, g, c0, c1; } first_part{-1, 0, 0, 0}, last_part{-1, 0, 0, 0};
 
   if (a.rope && threadIdx.x < kHeadDim / 2) {                  // while the first rows come
-    last_b = sm.start_b;
-    rope_cos_sin(sm.lens[a.B > kLensKept ? 0 : last_b], threadIdx.x, a.rope_pow,
-                 &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
+    last_b = w.b;
+    rope_cos_sin(w.r.p, threadIdx.x, a.rope_pow, &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
   }
   for (uint32_t k = 0;; ++k) {
     const Seg& sg = segs[k % kSegs];
@@ -839,43 +879,53 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     sm.last[i] = last;
   }
   math_sync();
-#pragma unroll 1
-  for (int i = 0; i < 2; ++i) {
-    if (!sm.last[i]) continue;
-    const Part q = i ? last_part : first_part;
-    const int h0 = q.g * a.G;
-    for (int e = threadIdx.x; e < a.G * (kHeadDim / 4); e += kMathThreads) {
-      const int r = e / (kHeadDim / 4), d = 4 * (e % (kHeadDim / 4));
-      // in the order of the ranges, whoever joins; the sink first
-      float M = __ldg(a.sink + h0 + r) * kLog2e, L = 1.f;
-      float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
-      constexpr int kAtOnce = 8;                               // partials in flight
-      for (int c = q.c0; c <= q.c1; c += kAtOnce) {
-        float2 ml[kAtOnce];
-        float4 v[kAtOnce];
+  // All warps join the one partial, or half of them each when both are due. A
+  // warp takes a head: lane i weighs partial c + i, then all lanes add up O.
+  const bool both = sm.last[0] && sm.last[1];
+  if (!sm.last[0] && !sm.last[1]) return;
+  const int part_warps = both ? kMathWarps / 2 : kMathWarps;
+  const Part q = (both ? warp >= part_warps : sm.last[1]) ? last_part : first_part;
+  for (int r = warp % part_warps; r < a.G; r += part_warps) {
+    float M = __ldg(a.sink + q.g * a.G + r) * kLog2e, L = 1.f;   // the sink first, then in order
+    float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = q.c0; c <= q.c1; c += 32) {
+      const int n = min(32, q.c1 - c + 1);
+      auto at = [&](int i) { return (2LL * (c + i) + (c + i == q.c0)) * 16 + r; };
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < n) ml = __ldcg(reinterpret_cast<const float2*>(A.part_ml) + at(lane));
+      constexpr int kAtOnce = 16;                              // rows of O in flight
+      float4 v[kAtOnce];
+      auto fetch = [&](int i0) {
 #pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const int cu = c + u;
-          const long long at = (2LL * cu + (cu == q.c0)) * 16 + r;
-          ml[u] = make_float2(-INFINITY, 0.f);
-          v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (cu <= q.c1) {
-            ml[u] = __ldcg(reinterpret_cast<const float2*>(A.part_ml) + at);
-            v[u] = __ldcg(reinterpret_cast<const float4*>(A.part_o + at * kHeadDim + d));
+        for (int i = 0; i < kAtOnce; ++i)
+          if (i0 + i < n)
+            v[i] = __ldcg(reinterpret_cast<const float4*>(A.part_o + at(i0 + i) * kHeadDim) + lane);
+      };
+      fetch(0);
+      float mx = ml.x;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      mx = fmaxf(mx, M);
+      const float mb = mx == -INFINITY ? 0.f : mx;
+      const float f = ex2_approx(M - mb), t = ex2_approx(ml.x - mb);
+      M = mx;
+      float l = ml.y * t;
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      L = L * f + l;
+      O.x *= f; O.y *= f; O.z *= f; O.w *= f;
+      for (int i0 = 0; i0 < n; i0 += kAtOnce) {
+        if (i0) fetch(i0);
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+          const float ti = __shfl_sync(0xffffffffu, t, (i0 + i) & 31);
+          if (i0 + i < n) {
+            O.x += v[i].x * ti; O.y += v[i].y * ti; O.z += v[i].z * ti; O.w += v[i].w * ti;
           }
         }
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) {
-          const float mn = fmaxf(M, ml[u].x), mb = mn == -INFINITY ? 0.f : mn;
-          const float f = ex2_approx(M - mb), t = ex2_approx(ml[u].x - mb);
-          M = mn;
-          L = L * f + ml[u].y * t;
-          O.x = O.x * f + v[u].x * t; O.y = O.y * f + v[u].y * t;
-          O.z = O.z * f + v[u].z * t; O.w = O.w * f + v[u].w * t;
-        }
       }
-      write_out(a, (long long)q.b * a.H + h0 + r, d, O, M, L);
     }
+    write_out(a, (long long)q.b * a.H + q.g * a.G + r, 4 * lane, O, M, L);
   }
 }
 
