@@ -17,17 +17,18 @@
 //     (m, l, O) and the last of a pair's segments to finish joins them. The plan
 //     is made on the device by every block (a scan over lens), so a captured
 //     call follows its lengths and nothing but lens decides who sums what.
-//   * Loads. Four warps stream K and V of the range, a block each in turn, through
+//   * Loads. Two warps stream K and V of the range, a block each in turn, through
 //     a ring of shared memory with TMA, across segment borders, so that the ring
 //     fills while the math warps finish one segment and start the next. (Issuing a
 //     copy costs a warp 130 cycles or more: over 16-slot pages of e4m3 one warp
-//     alone took as long as its blocks' share of the HBM bandwidth twice over.) A tensor map in five
-//     dimensions (64 channels, slot, channel half, head, page) takes any page,
-//     head and token strides; a box is the largest power of two of slots that
-//     divides the page, at most 64, so no box crosses a page. With the rings of
-//     148 SMs full, 19 MB are in flight and any load waits ~3 us behind them, so
-//     the first of these warps brings everything else a segment needs (the q rows, the new
-//     row, the page of its slot, scales, sinks) up to four segments ahead.
+//     alone took as long as its blocks' share of the HBM bandwidth twice over.)
+//     A tensor map in five dimensions (64 channels, slot, channel half, head,
+//     page) takes any page, head and token strides; a box is the largest power of
+//     two of slots that divides the page, at most 64, so no box crosses a page.
+//   * Rows. With the rings of 148 SMs full, 19 MB are in flight and any load
+//     waits ~3 us behind them. Two more warps therefore fetch, normalise and
+//     rotate the q rows and the new row of the coming segments, up to four ahead,
+//     and lay q out as the products take it.
 //   * Math. Eight warps take the blocks in turn, 32 keys and eight query heads a
 //     warp (up to 8 heads: four pairs of warps, a block each; 9 to 16: two groups
 //     of four), on mma.sync m16n8k16 with FP32 accumulation. S takes q as two 16-bit parts, hi in rows 0-7 and lo in rows 8-15 of
@@ -50,9 +51,10 @@ namespace {
 constexpr int kBlk = 64;                     // positions per unit of work
 constexpr int kKeys = 32;                    // of a block, per warp
 constexpr int kMathWarps = 8;
-constexpr int kLoadWarps = 4;                // block n is loaded by warp n % 4
+constexpr int kLoadWarps = 2;                // block n is loaded by warp n % 2
+constexpr int kRowWarps = 2;                 // four half-warps, a row each in turn
 constexpr int kMathThreads = 32 * kMathWarps;
-constexpr int kThreads = kMathThreads + 32 * kLoadWarps;
+constexpr int kThreads = kMathThreads + 32 * (kLoadWarps + kRowWarps);
 constexpr int kMergeRow = kHeadDim + 4;      // O, m, l (and two unused): rows stay 16-byte aligned
 constexpr int kSegs = 4;                     // segments described ahead
 constexpr int kLensKept = 512;               // rows whose lens a block keeps
@@ -60,9 +62,15 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kRescale = 8.0f;             // log2 units
 
-// What the math warps need of a segment, brought by the loading warp.
+// What the math warps need of a segment, made by the row warps.
+template <int NG>
 struct __align__(16) Seg {
-  __nv_bfloat16 q[16 * kHeadDim], k[kHeadDim], v[kHeadDim];    // raw rows (k, v: last segment)
+  // A operand of S, 8 heads and 16 channels each: rows 0-7 the hi parts, rows
+  // 8-15 the lo parts of the heads' q_hat (log2 units), as the lanes hold it
+  uint4 frag[NG * 8 * 32];
+  float vnew[kHeadDim];                      // the new value as the cache stores it, times scale
+  uint4 kbits[16], vbits[16];                // the new row's bits, a lane's channels each
+  float snew[16];                            // the new token's scores, log2 units
   float sink[16], ks, vs;
   long long dst;                             // the new token's slot (KV head 0), -1: no page
   int b, g;
@@ -71,41 +79,38 @@ struct __align__(16) Seg {
   int c0, c1;                                // the ranges that share the pair
   int final;                                 // the range's last segment
 };
+constexpr int kMaxBars = 20;
 struct Small {
-  uint64_t full[16], empty[16], seg_full[kSegs], seg_empty[kSegs];
-  int bad[16];                               // the stage lacks a page
-  float cs[kHeadDim / 2], sn[kHeadDim / 2];
-  float knew[kHeadDim], vnew[kHeadDim];      // the new row as the cache stores it, times scale
-  uint4 kbits[16], vbits[16];                // and its bits, a lane's channels each
-  float snew[16];                            // its scores, log2 units
+  uint64_t full[kMaxBars], empty[kMaxBars], seg_full[kSegs], seg_empty[kSegs];
+  int bad[kMaxBars];                         // the block lacks a page
   long long scan[kThreads / 32], start_off;
   int start_b, abort_flag, last[2];
   int lens[kLensKept];
 };
-// Shared memory: [ring | merge rows of the 8 warps (q rows before that) | q
-// fragments | segments | Small].
+// Shared memory: [ring | merge rows of the 8 warps | segments | Small].
 // NG: query heads in groups of 8 (1: G <= 8, 2: G <= 16).
 template <int NG, bool kF8>
 struct Cfg {
   static constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
   static constexpr int kStageBytes = 2 * kBlk * kRowBytes;          // K, then V
-  // A multiple of the groups: the groups take the blocks in turn, so each stage
-  // then belongs to one group, which sees every phase of its barriers. In any
-  // other ring a group's parity wait could be two phases behind and pass early.
   // A pair's fixed cost in units. 201 rows of up to 2513 keys, nine heads to a KV
   // head, cost 0, 4, 8, 12: 54.1, 43.8, 44.8, - us in bf16, 58.4, 45.8, 44.9, 46.3
   // in e4m3; 250 rows of up to 900: 71.8, 53.2, 54.2, - and 76.0, 53.1, 47.5, 47.3.
   static constexpr int kCost = kF8 ? 8 : 4;
   static constexpr int kGroupWarps = 2 * NG, kGroups = kMathWarps / kGroupWarps;
-  static constexpr int kStages = kF8 ? 8 : 4;
-  static_assert(kStages % kGroups == 0 && kStages <= 16, "see above");
-  static_assert(kStages % kLoadWarps == 0, "a stage belongs to one loading warp");
+  // Block u goes to stage u % kStages, to group u % kGroups, and has the barriers
+  // u % kBars: a multiple of the stages, the groups and the loading warps, so each
+  // barrier belongs to one group and one loading warp, which see every phase of
+  // it. Were the barriers the stages', a parity wait of a group that does not
+  // divide them could be two phases behind and pass early.
+  static constexpr int kStages = (NG == 1 ? 5 : 4) * (kF8 ? 2 : 1);
+  static constexpr int kBars = NG == 1 ? 20 : 8;
+  static_assert(kBars % kStages == 0 && kBars % kGroups == 0 && kBars % kLoadWarps == 0 &&
+                kBars <= kMaxBars, "see above");
   static constexpr int kMergeBytes = kMathWarps * 8 * kMergeRow * 4;
-  static constexpr int kFragBytes = NG * 8 * 32 * 16;
   static constexpr int kOffMerge = kStages * kStageBytes;
-  static constexpr int kOffFrag = kOffMerge + kMergeBytes;
-  static constexpr int kOffSegs = kOffFrag + kFragBytes;
-  static constexpr int kOffSmall = kOffSegs + kSegs * (int)sizeof(Seg);
+  static constexpr int kOffSegs = kOffMerge + kMergeBytes;
+  static constexpr int kOffSmall = kOffSegs + kSegs * (int)sizeof(Seg<NG>);
   static constexpr int kSmemBytes = kOffSmall + (int)sizeof(Small) + 1024;   // + alignment
   // P = 2^(s - m + bias): fp16 P starts at 2^-24, so its rows are lifted
   static constexpr float kBias = kF8 ? 6.f : 0.f;
@@ -172,8 +177,6 @@ struct Walk {
     }
     return cut();
   }
-  // Whether this is the range's last segment: what may follow is less than a block.
-  __device__ bool final() const { return left - units <= cost; }
 };
 
 // ------------------------------------------------------------------ small pieces
@@ -186,14 +189,6 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* m, 
       "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
       " [%0], [%1, {%3, %4, %3, %5, %6}], [%2];" ::"r"(dst),
       "l"(reinterpret_cast<uint64_t>(m)), "r"(bar), "r"(0), "r"(slot), "r"(head), "r"(page)
-      : "memory");
-}
-// Untiled copy of bytes (a multiple of 16, both addresses 16-byte aligned).
-__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes,
-                                          uint32_t bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
-          "r"(dst), "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void math_sync() {
@@ -278,19 +273,18 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* merge = reinterpret_cast<float*>(smem + C::kOffMerge);
-  uint4* frag = reinterpret_cast<uint4*>(smem + C::kOffFrag);
-  Seg* segs = reinterpret_cast<Seg*>(smem + C::kOffSegs);
+  Seg<NG>* segs = reinterpret_cast<Seg<NG>*>(smem + C::kOffSegs);
   Small& sm = *reinterpret_cast<Small*>(smem + C::kOffSmall);
   const PagedDecodeLaunch& a = A.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == kMathThreads) {
-    for (int s = 0; s < C::kStages; ++s) {
+    for (int s = 0; s < C::kBars; ++s) {
       mbar_init(smem_u32(&sm.full[s]), 1);
       mbar_init(smem_u32(&sm.empty[s]), C::kGroupWarps);
     }
     for (int s = 0; s < kSegs; ++s) {
-      mbar_init(smem_u32(&sm.seg_full[s]), 1);
+      mbar_init(smem_u32(&sm.seg_full[s]), kRowWarps);
       mbar_init(smem_u32(&sm.seg_empty[s]), kMathWarps);
     }
     sm.abort_flag = 0;
@@ -387,13 +381,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   if (!w.cut()) return;                      // not a block in this range
   const WaitCtx wc{&sm.abort_flag, a.status, kStatusTimeoutFwd};
 
-  if (warp >= kMathWarps) {
+  if (warp >= kMathWarps + kRowWarps) {
     // ---------------------------------------------------------------- loads
     const int nbox = kBlk / A.box;                             // 1, 2 or 4 boxes a block
     const uint32_t box_bytes = (uint32_t)A.box * C::kRowBytes;
-    const uint32_t lw = warp - kMathWarps;                     // takes blocks n % 4 == lw
-    const bool describes = lw == kLoadWarps - 1;               // not the one with block 0
-    uint32_t n = 0, k = 0, issued = 0;                         // issued: its last block + 1
+    const uint32_t lw = warp - kMathWarps - kRowWarps;         // takes blocks n % kLoadWarps == lw
+    uint32_t n = 0, issued = 0;                                // issued: its last block + 1
     bool ok = true;
     // The table is read 32 boxes at a time and ahead: lane i holds the page and
     // slot of box at + i of a segment (-2: nothing visible; -1: a bad page).
@@ -405,86 +398,30 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       const int32_t* row = a.c.table + v.b * a.c.table_stride;
       return Box{need ? max(__ldg(row + col), -1) : -2, pos - col * a.c.P};
     };
-    // What a segment needs besides keys, requested one segment ahead.
-    struct Ahead { Box box; int page, slot; float sink, ks, vs; };
-    auto look = [&](const Walk& v) {
-      Ahead h;
-      h.box = fetch(v, 0);
-      if (describes) {
-        const int col = page_col(A, v.r.p);
-        h.page = __ldg(a.c.table + v.b * a.c.table_stride + col);
-        h.slot = v.r.p - col * a.c.P;
-        h.sink = lane < a.G ? __ldg(a.sink + v.g * a.G + lane) : 0.f;
-        h.ks = kF8 && a.c.k_scale ? __ldg(a.c.k_scale + v.g) : 1.f;
-        h.vs = kF8 && a.c.v_scale ? __ldg(a.c.v_scale + v.g) : 1.f;
-      }
-      return h;
-    };
-    Ahead h = look(w);
+    Box next = fetch(w, 0);
     while (true) {
-      // ---- describe the segment
-      if (describes) {
-        Seg& sg = segs[k % kSegs];
-        if (k >= kSegs)
-          ok = mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc);
-        if (!ok) break;
-        const bool owner = w.blk + w.len == w.r.n;
-        const uint32_t bar = smem_u32(&sm.seg_full[k % kSegs]);
-        const uint32_t q_bytes = (uint32_t)a.G * kHeadDim * 2, row = kHeadDim * 2;
-        if (lane == 0) {                                       // their bytes may land before
-          bulk_load(smem_u32(sg.q), a.q + w.b * a.q_stride + (long long)w.g * a.G * kHeadDim,
-                    q_bytes, bar);                             // the barrier expects them
-          if (owner) {
-            bulk_load(smem_u32(sg.k), a.k + w.b * a.k_stride + w.g * kHeadDim, row, bar);
-            bulk_load(smem_u32(sg.v), a.v + w.b * a.v_stride + w.g * kHeadDim, row, bar);
-          }
-          sg.b = w.b;
-          sg.g = w.g;
-          sg.blk = w.blk;
-          sg.len = w.len;
-          sg.n = w.r.n;
-          sg.p = w.r.p;
-          sg.lo = w.r.lo;
-          sg.first = w.r.first;
-          sg.final = w.final();
-          if (w.len < w.r.n) {
-            // the pair's first and last block are units of these ranges
-            const long long end = u_end - w.left + w.units;
-            const long long last = end - 1 + (w.r.n - w.blk - w.len);
-            sg.c0 = (int)quotient(last - (w.r.n - 1), share);
-            sg.c1 = (int)quotient(last, share);
-          }
-          sg.ks = h.ks;
-          sg.vs = h.vs;
-          sg.dst = (unsigned)h.page < (unsigned)a.c.num_pages
-                       ? h.page * a.c.page_stride + h.slot * a.c.token_stride : -1;
-        }
-        if (lane < 16) sg.sink[lane] = h.sink;
-        __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(bar, q_bytes + (owner ? 2 * row : 0));
-      }
-      ++k;
-      // ---- its keys
       Walk nx = w;
-      Box cur = h.box, ahead{};
+      Box cur = next, ahead{};
       bool more = false, looked = false;
       auto look_ahead = [&] {                                  // after the first block's copies
         ahead = fetch(w, 32);
         more = nx.next(a, sm.lens);
-        if (more) h = look(nx);
+        if (more) next = fetch(nx, 0);
         looked = true;
       };
       int batch = 0;
       for (int j = (int)((lw - n) & (kLoadWarps - 1)); j < w.len; j += kLoadWarps) {
         const int i = j * nbox;                                // the block's first box
-        if (i / 32 != batch) {                                 // a turn has at most 16 boxes
+        if (i / 32 != batch) {                                 // a turn has at most 8 boxes
           cur = ahead;
           ahead = fetch(w, 32 * (++batch + 1));
         }
         const uint32_t u = n + j;
-        const int s = u % C::kStages;
-        if (u >= C::kStages)
-          ok = mbar_wait_warp(smem_u32(&sm.empty[s]), (u / C::kStages - 1) & 1, wc);
+        const int s = u % C::kStages, bar = u % C::kBars;
+        if (u >= C::kStages) {                                 // the stage's last block is done
+          const uint32_t d = u - C::kStages;
+          ok = mbar_wait_warp(smem_u32(&sm.empty[d % C::kBars]), (d / C::kBars) & 1, wc);
+        }
         if (!ok) break;
         issued = u + 1;
         const int page = __shfl_sync(0xffffffffu, cur.page, (i + lane) & 31);
@@ -493,9 +430,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         const bool good = need && (unsigned)page < (unsigned)a.c.num_pages;
         const unsigned good_mask = __ballot_sync(0xffffffffu, good);
         const unsigned bad_mask = __ballot_sync(0xffffffffu, need && !good);
-        const uint32_t full = smem_u32(&sm.full[s]);
+        const uint32_t full = smem_u32(&sm.full[bar]);
         if (lane == 0) {
-          sm.bad[s] = bad_mask != 0;
+          sm.bad[bar] = bad_mask != 0;
           if (bad_mask) atomicOr(a.status, kStatusDecodeRange);
           mbar_arrive_expect_tx(full, 2 * __popc(good_mask) * box_bytes);
         }
@@ -519,16 +456,150 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const WaitCtx drain{&no_abort, a.status, kStatusTimeoutFwd};
     for (uint32_t u = issued > C::kStages ? issued - C::kStages : 0; u < issued; ++u)
       if (u % kLoadWarps == lw)
-        mbar_wait_warp(smem_u32(&sm.full[u % C::kStages]), (u / C::kStages) & 1, drain);
-    if (describes && ok)                                       // (a failed wait described none)
-      for (uint32_t i = k > kSegs ? k - kSegs : 0; i < k; ++i)
-        mbar_wait_warp(smem_u32(&sm.seg_full[i % kSegs]), (i / kSegs) & 1, drain);
+        mbar_wait_warp(smem_u32(&sm.full[u % C::kBars]), (u / C::kBars) & 1, drain);
+    return;
+  }
+
+  if (warp >= kMathWarps) {
+    // ---------------------------------------------------------------- rows
+    const int hw = (threadIdx.x - kMathThreads) >> 4, l16 = lane & 15;   // half-warp, its lane
+    constexpr int kHw = 2 * kRowWarps, kRows = 8 * NG / kHw;   // rows of a half-warp: hw + kHw i
+    const bool lead = warp == kMathWarps;
+    float wq[8], wk[8], cs[8], sn[8];
+    load8(a.wq + 8 * l16, wq);
+    load8(a.wk + 8 * l16, wk);
+    // What a segment takes from memory, requested one segment ahead.
+    struct Raw { uint4 q[kRows], k, v; int page, slot; float sink, ks, vs; };
+    auto look = [&](const Walk& v) {
+      Raw h;
+      const __nv_bfloat16* q = a.q + v.b * a.q_stride + (long long)v.g * a.G * kHeadDim + 8 * l16;
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = hw + kHw * i;
+        h.q[i] = r < a.G ? *reinterpret_cast<const uint4*>(q + r * kHeadDim) : make_uint4(0, 0, 0, 0);
+      }
+      h.k = *reinterpret_cast<const uint4*>(a.k + v.b * a.k_stride + v.g * kHeadDim + 8 * l16);
+      h.v = *reinterpret_cast<const uint4*>(a.v + v.b * a.v_stride + v.g * kHeadDim + 8 * l16);
+      const int col = page_col(A, v.r.p);
+      h.page = __ldg(a.c.table + v.b * a.c.table_stride + col);
+      h.slot = v.r.p - col * a.c.P;
+      h.sink = lane < a.G ? __ldg(a.sink + v.g * a.G + lane) : 0.f;
+      h.ks = kF8 && a.c.k_scale ? __ldg(a.c.k_scale + v.g) : 1.f;
+      h.vs = kF8 && a.c.v_scale ? __ldg(a.c.v_scale + v.g) : 1.f;
+      return h;
+    };
+    Raw h = look(w);
+    int last_b = -1;
+    for (uint32_t k = 0;; ++k) {
+      Walk nx = w;
+      const bool more = nx.next(a, sm.lens);
+      const Raw cur = h;
+      if (more) h = look(nx);
+      if (a.rope && w.b != last_b) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          rope_cos_sin(w.r.p, 8 * (l16 & 7) + e, a.rope_pow, &cs[e], &sn[e]);
+        last_b = w.b;
+      }
+      Seg<NG>& sg = segs[k % kSegs];
+      if (k >= kSegs &&
+          !mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc))
+        break;
+      const bool owner = w.blk + w.len == w.r.n;
+      float kn[8];                                             // as the cache stores it
+      if (owner) {                                             // every half-warp the same row
+        float y[8];
+        unpack8(cur.k, kn);
+        unpack8(cur.v, y);
+        row_prologue(kn, wk, cs, sn, a.rope, a.eps);
+        uint4 kb, vb = cur.v;
+        if constexpr (kF8) {
+          const uint2 bk = pack_e4m3_row(kn, cur.ks), bv = pack_e4m3_row(y, cur.vs);
+          kb = make_uint4(bk.x, bk.y, 0, 0);
+          vb = make_uint4(bv.x, bv.y, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            kn[e] = e4m3_to_f32(((e < 4 ? bk.x : bk.y) >> (8 * (e & 3))) & 0xff) * cur.ks;
+            y[e] = e4m3_to_f32(((e < 4 ? bv.x : bv.y) >> (8 * (e & 3))) & 0xff) * cur.vs;
+          }
+        } else {
+          kb = pack_bf16_row(kn);
+          unpack8(kb, kn);
+        }
+        if (hw == 0) {
+          sg.kbits[l16] = kb;
+          sg.vbits[l16] = vb;
+          *reinterpret_cast<float4*>(&sg.vnew[8 * l16]) = make_float4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<float4*>(&sg.vnew[8 * l16 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const int r = hw + kHw * i;
+        float x[8];
+        unpack8(cur.q[i], x);
+        row_prologue(x, wq, cs, sn, a.rope, a.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = r < a.G ? x[e] * A.scale_log2 : 0.f;   // zero past G
+        if (owner) {                                           // the new token's score
+          float z = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) z += x[e] * kn[e];
+#pragma unroll
+          for (int o = 8; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
+          if (l16 == 0) sg.snew[r] = z;
+        }
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split_pair<kF8>(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
+        // Channels 8 l16 .. are half of chunk l16 / 2. bf16: the lanes of head r
+        // (4 r + tig) hold channels 2 tig, + 1 and 2 tig + 8, + 9 of a chunk.
+        // Over e4m3 a lane's four bytes are channels 4 tig .., so q takes the
+        // chunk's channels in that order as well.
+        uint4* f = sg.frag + ((r >> 3) * 8 + (l16 >> 1)) * 32 + 4 * (r & 7);
+        if constexpr (kF8) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            f[2 * (l16 & 1) + e] = make_uint4(hi[2 * e], lo[2 * e], hi[2 * e + 1], lo[2 * e + 1]);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            reinterpret_cast<uint2*>(f + e)[l16 & 1] = make_uint2(hi[e], lo[e]);
+        }
+      }
+      if (lead && lane < 16) sg.sink[lane] = cur.sink;
+      if (lead && lane == 0) {
+        sg.ks = cur.ks;
+        sg.vs = cur.vs;
+        sg.dst = (unsigned)cur.page < (unsigned)a.c.num_pages
+                     ? cur.page * a.c.page_stride + cur.slot * a.c.token_stride : -1;
+        sg.b = w.b;
+        sg.g = w.g;
+        sg.blk = w.blk;
+        sg.len = w.len;
+        sg.n = w.r.n;
+        sg.p = w.r.p;
+        sg.lo = w.r.lo;
+        sg.first = w.r.first;
+        sg.final = !more;
+        if (w.len < w.r.n) {
+          // the pair's first and last block are units of these ranges
+          const long long end = u_end - w.left + w.units;
+          const long long last = end - 1 + (w.r.n - w.blk - w.len);
+          sg.c0 = (int)quotient(last - (w.r.n - 1), share);
+          sg.c1 = (int)quotient(last, share);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sm.seg_full[k % kSegs]));
+      if (!more) break;
+      w = nx;
+    }
     return;
   }
 
   // ------------------------------------------------------------------ math
   const int gid = lane >> 2, tig = lane & 3;
-  const int half = threadIdx.x >> 4, l16 = threadIdx.x & 15;   // 16 half-warps
   const int group = warp / C::kGroupWarps;                     // takes blocks n % kGroups == group
   const int key0 = kKeys * (warp & 1);                         // of the block
   const int t8 = NG == 1 ? 0 : 8 * ((warp >> 1) & 1);          // the warp's first query head
@@ -540,99 +611,22 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     chunk_at[c] = (uint32_t)((key0 + 16 * c) / A.box) * A.box * C::kRowBytes +
                   (uint32_t)((key0 + 16 * c) % A.box) * 128;
   const uint32_t half_bytes = (uint32_t)A.box * 128;           // bf16: channels 64..127
-  float wq[8], wk[8];
-  load8(a.wq + 8 * l16, wq);
-  load8(a.wk + 8 * l16, wk);
   uint32_t n = 0;
-  int last_b = -1;
   bool ok = true;
   // Partials, with their pair's ranges c0 .. c1: of a pair that began in an
   // earlier range (first), and of one that goes on in a later range (last).
   struct Part { int b, g, c0, c1; } first_part{-1, 0, 0, 0}, last_part{-1, 0, 0, 0};
 
-  if (a.rope && threadIdx.x < kHeadDim / 2) {                  // while the first rows come
-    last_b = w.b;
-    rope_cos_sin(w.r.p, threadIdx.x, a.rope_pow, &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
-  }
   for (uint32_t k = 0;; ++k) {
-    const Seg& sg = segs[k % kSegs];
-    if (ok) ok = mbar_wait_warp(smem_u32(&sm.seg_full[k % kSegs]), (k / kSegs) & 1, wc);
-    if (ok && a.rope && sg.b != last_b && threadIdx.x < kHeadDim / 2)
-      rope_cos_sin(sg.p, threadIdx.x, a.rope_pow, &sm.cs[threadIdx.x], &sm.sn[threadIdx.x]);
-    if (!math_sync_and(ok)) break;                             // table; merge area free
-    last_b = sg.b;
-    const int len = sg.len, p = sg.p, lo = sg.lo;
-    const bool owner = sg.blk + len == sg.n;                   // this segment has the new token
+    const Seg<NG>& sg = segs[k % kSegs];
+    ok = mbar_wait_warp(smem_u32(&sm.seg_full[k % kSegs]), (k / kSegs) & 1, wc) && ok;
+    // A segment is entered by all warps or none: len stays 0 where its wait ran out.
+    const int len = ok ? sg.len : 0, p = sg.p, lo = sg.lo;
+    const bool owner = sg.blk + sg.len == sg.n;                // this segment has the new token
     const float ks = sg.ks;
-
-    // ---- q rows (half-warps 0 .. G-1) and, in the last segment, the new row
-    float (*qs)[kHeadDim] = reinterpret_cast<float (*)[kHeadDim]>(merge);
-    if (half < 8 * NG) {                                       // whole warps; zero past G
-      float x[8] = {};
-      if (half < a.G) load8(sg.q + half * kHeadDim + 8 * l16, x);
-      row_prologue(x, wq, sm.cs, sm.sn, a.rope, a.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = half < a.G ? x[e] * A.scale_log2 : 0.f;
-      *reinterpret_cast<float4*>(&qs[half][8 * l16]) = make_float4(x[0], x[1], x[2], x[3]);
-      *reinterpret_cast<float4*>(&qs[half][8 * l16 + 4]) = make_float4(x[4], x[5], x[6], x[7]);
-    }
-    if (owner && warp == kMathWarps - 1) {                     // both half-warps the same row
-      float x[8], y[8];
-      load8(sg.k + 8 * l16, x);
-      load8(sg.v + 8 * l16, y);
-      row_prologue(x, wk, sm.cs, sm.sn, a.rope, a.eps);
-      if (lane < 16) {
-        if constexpr (kF8) {
-          const uint2 bk = pack_e4m3_row(x, ks), bv = pack_e4m3_row(y, sg.vs);
-          sm.kbits[lane] = make_uint4(bk.x, bk.y, 0, 0);
-          sm.vbits[lane] = make_uint4(bv.x, bv.y, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            x[e] = e4m3_to_f32(((e < 4 ? bk.x : bk.y) >> (8 * (e & 3))) & 0xff) * ks;
-            y[e] = e4m3_to_f32(((e < 4 ? bv.x : bv.y) >> (8 * (e & 3))) & 0xff) * sg.vs;
-          }
-        } else {
-          sm.kbits[lane] = pack_bf16_row(x);
-          sm.vbits[lane] = pack_bf16_row(y);
-          unpack8(sm.kbits[lane], x);
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          sm.knew[8 * l16 + e] = x[e];
-          sm.vnew[8 * l16 + e] = y[e];
-        }
-      }
-    }
-    math_sync();
-
-    // ---- A operand of S: rows 0-7 the hi parts, rows 8-15 the lo parts of 8 heads.
-    // Warp kk lays out the fragments of the 16 channels 16 kk .., for all warps.
-    // Over e4m3 a lane's four bytes of such a chunk are channels 4 tig ..,
-    // so the chunk's channels are taken in that order by q as well.
-#pragma unroll
-    for (int t = 0; t < NG; ++t) {
-      const float* q = qs[8 * t + gid] + 16 * warp;
-      const float2 u = *reinterpret_cast<const float2*>(q + (kF8 ? 4 * tig : 2 * tig));
-      const float2 v = *reinterpret_cast<const float2*>(q + (kF8 ? 4 * tig + 2 : 2 * tig + 8));
-      uint4 f;
-      split_pair<kF8>(u.x, u.y, f.x, f.y);
-      split_pair<kF8>(v.x, v.y, f.z, f.w);
-      frag[(t * 8 + warp) * 32 + lane] = f;
-    }
-    if (owner) {                                               // the new token's scores
-      for (int h = warp; h < a.G; h += kMathWarps) {
-        const float4 q = *reinterpret_cast<const float4*>(&qs[h][4 * lane]);
-        const float4 kn = *reinterpret_cast<const float4*>(&sm.knew[4 * lane]);
-        float z = q.x * kn.x + q.y * kn.y + q.z * kn.z + q.w * kn.w;
-#pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-        if (lane == 0) sm.snew[h] = z;
-      }
-    }
-    math_sync();                                               // qs is free for the merge
     uint4 qf[8];
 #pragma unroll
-    for (int kk = 0; kk < 8; ++kk) qf[kk] = frag[(t8 + kk) * 32 + lane];
+    for (int kk = 0; kk < 8; ++kk) qf[kk] = sg.frag[(t8 + kk) * 32 + lane];
 
     // ---- the segment's keys
     // o: O^T, 8 m-tiles of 16 channels x 8 heads; m (log2 units, less kBias) and
@@ -643,10 +637,10 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int base = (sg.first + sg.blk) * kBlk + key0;
     for (int j = (int)((group - n) & (C::kGroups - 1)); j < len; j += C::kGroups) {
       const uint32_t u = n + j;
-      const int s = u % C::kStages;
-      if (ok) ok = mbar_wait_warp(smem_u32(&sm.full[s]), (u / C::kStages) & 1, wc);
+      const int s = u % C::kStages, bar = u % C::kBars;
+      if (ok) ok = mbar_wait_warp(smem_u32(&sm.full[bar]), (u / C::kBars) & 1, wc);
       const int pos0 = base + j * kBlk;                        // the warp's first key
-      if (sm.bad[s]) l = NAN;
+      if (sm.bad[bar]) l = NAN;
       if (pos0 < p && pos0 + kKeys > lo) {
         const bool edge = pos0 < lo || pos0 + kKeys > p;
         const uint32_t st = ring + s * C::kStageBytes;
@@ -771,11 +765,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sm.empty[s]));
+      if (lane == 0) mbar_arrive(smem_u32(&sm.empty[bar]));
     }
     n += len;
 
     // ---- join the warps
+    if (!math_sync_and(ok)) break;                             // the merge rows are free
     {
       float* rows = merge + warp * 8 * kMergeRow;
       l += __shfl_xor_sync(0xffffffffu, l, 1);
@@ -806,7 +801,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         const int wp = NG == 1 ? i : 4 * (i >> 1) + 2 * (r >> 3) + (i & 1);
         return merge + (wp * 8 + (r & 7)) * kMergeRow;
       };
-      float M = owner ? sm.snew[r] : -INFINITY;
+      float M = owner ? sg.snew[r] : -INFINITY;
 #pragma unroll
       for (int i = 0; i < kMathWarps / NG; ++i) M = fmaxf(M, part(i)[kHeadDim]);
       const float s2 = whole ? sg.sink[r] * kLog2e : -INFINITY;
@@ -827,8 +822,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         O.x *= vs; O.y *= vs; O.z *= vs; O.w *= vs;
       }
       if (owner) {
-        const float f = ex2_approx(sm.snew[r] - Mb);
-        const float4 v = *reinterpret_cast<const float4*>(&sm.vnew[d]);
+        const float f = ex2_approx(sg.snew[r] - Mb);
+        const float4 v = *reinterpret_cast<const float4*>(&sg.vnew[d]);
         L += no_page ? NAN : f;
         O.x += v.x * f; O.y += v.y * f; O.z += v.z * f; O.w += v.w * f;
       }
@@ -843,8 +838,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     if (owner && warp == kMathWarps - 1 && lane < 16 && !no_page) {
       const long long off = sg.dst + sg.g * a.c.head_stride;
-      store_bits(a.c, a.c.k, off, sm.kbits[lane]);
-      store_bits(a.c, a.c.v, off, sm.vbits[lane]);
+      store_bits(a.c, a.c.k, off, sg.kbits[lane]);
+      store_bits(a.c, a.c.v, off, sg.vbits[lane]);
     }
     if (no_page && threadIdx.x == 0) atomicOr(a.status, kStatusDecodeRange);
     if (!whole) {                                              // to be joined at the end

@@ -74,12 +74,12 @@ __device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
 
 // RMSNorm with weight w, then (rope) the rotation of channel j with j + 64. A
 // half-warp owns the row, lane l of it channels 8l .. 8l+7, whose partners are
-// in lane l ^ 8. cs, sn: the 64 cosines and sines of the row's position. The
-// whole warp calls it (full-mask shuffles). The append and the decode kernel
-// use this one function, so both store the same bits for the same token.
+// in lane l ^ 8; cs, sn: the cosines and sines of the lane's channels (angles
+// 8 (l & 7) ..). The whole warp calls it (full-mask shuffles). The append and
+// the decode kernel use this one function, so both store the same bits for the
+// same token.
 __device__ __forceinline__ void row_prologue(float (&x)[8], const float (&w)[8], const float* cs,
                                              const float* sn, bool rope, float eps) {
-  const int l = threadIdx.x & 15;
   float ss = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
@@ -89,12 +89,11 @@ __device__ __forceinline__ void row_prologue(float (&x)[8], const float (&w)[8],
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
   if (rope) {
-    const int j0 = 8 * (l & 7);
+    const float sign = (threadIdx.x & 8) ? 1.f : -1.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float partner = __shfl_xor_sync(0xffffffffu, x[e], 8);
-      const float c = cs[j0 + e], s = sn[j0 + e];
-      x[e] = l < 8 ? x[e] * c - partner * s : x[e] * c + partner * s;
+      x[e] = x[e] * cs[e] + partner * (sign * sn[e]);
     }
   }
 }

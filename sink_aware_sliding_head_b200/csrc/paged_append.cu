@@ -66,7 +66,7 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedAppen
       load8(a.k + t * a.k_stride + g * kHeadDim + 8 * l, x);
       load8(a.v + t * a.v_stride + g * kHeadDim + 8 * l, y);
     }
-    row_prologue(x, w, cs[i], sn[i], a.rope, a.eps);
+    row_prologue(x, w, &cs[i][8 * (l & 7)], &sn[i][8 * (l & 7)], a.rope, a.eps);
     if (live) {
       const long long off = slot[i] + g * a.c.head_stride;
       store_row(a.c, a.c.k, off, x, a.c.k_scale ? __ldg(a.c.k_scale + g) : 1.f);
