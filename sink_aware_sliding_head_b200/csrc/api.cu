@@ -685,7 +685,7 @@ extern "C" flint_status_t flint_attn_paged_append(
   L.v = static_cast<const __nv_bfloat16*>(v);
   L.wk = static_cast<const __nv_bfloat16*>(k_norm_w);
   L.cu = cu_new_lens; L.lens = cache_lens; L.status = status;
-  return cuda_status(launch_paged_append(L, reinterpret_cast<cudaStream_t>(stream)));
+  return cuda_status(launch_paged_append(L, sm_count(), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 extern "C" size_t flint_attn_decode_paged_workspace_bytes(

@@ -69,7 +69,7 @@ struct __align__(16) Seg {
   // 8-15 the lo parts of the heads' q_hat (log2 units), as the lanes hold it
   uint4 frag[NG * 8 * 32];
   float vnew[kHeadDim];                      // the new value as the cache stores it, times scale
-  uint4 kbits[16], vbits[16];                // the new row's bits, a lane's channels each
+  RowBits kbits[16], vbits[16];              // the new row as the cache stores it, by lane
   float snew[16];                            // the new token's scores, log2 units
   float sink[16], ks, vs;
   long long dst;                             // the new token's slot (KV head 0), -1: no page
@@ -465,21 +465,23 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int hw = (threadIdx.x - kMathThreads) >> 4, l16 = lane & 15;   // half-warp, its lane
     constexpr int kHw = 2 * kRowWarps, kRows = 8 * NG / kHw;   // rows of a half-warp: hw + kHw i
     const bool lead = warp == kMathWarps;
-    float wq[8], wk[8], cs[8], sn[8];
-    load8(a.wq + 8 * l16, wq);
-    load8(a.wk + 8 * l16, wk);
+    const RowPart wq = unpack_row(load_row(a.wq)), wk = unpack_row(load_row(a.wk));
+    float cs[4], sn[4];
+    double f[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = rope_turns(4 * l16 + e, a.rope_pow);
     // What a segment takes from memory, requested one segment ahead.
-    struct Raw { uint4 q[kRows], k, v; int page, slot; float sink, ks, vs; };
+    struct Raw { RowBits q[kRows], k, v; int page, slot; float sink, ks, vs; };
     auto look = [&](const Walk& v) {
       Raw h;
-      const __nv_bfloat16* q = a.q + v.b * a.q_stride + (long long)v.g * a.G * kHeadDim + 8 * l16;
+      const __nv_bfloat16* q = a.q + v.b * a.q_stride + (long long)v.g * a.G * kHeadDim;
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = hw + kHw * i;
-        h.q[i] = r < a.G ? *reinterpret_cast<const uint4*>(q + r * kHeadDim) : make_uint4(0, 0, 0, 0);
+        h.q[i] = r < a.G ? load_row(q + r * kHeadDim) : RowBits{};
       }
-      h.k = *reinterpret_cast<const uint4*>(a.k + v.b * a.k_stride + v.g * kHeadDim + 8 * l16);
-      h.v = *reinterpret_cast<const uint4*>(a.v + v.b * a.v_stride + v.g * kHeadDim + 8 * l16);
+      h.k = load_row(a.k + v.b * a.k_stride + v.g * kHeadDim);
+      h.v = load_row(a.v + v.b * a.v_stride + v.g * kHeadDim);
       const int col = page_col(A, v.r.p);
       h.page = __ldg(a.c.table + v.b * a.c.table_stride + col);
       h.slot = v.r.p - col * a.c.P;
@@ -497,8 +499,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (more) h = look(nx);
       if (a.rope && w.b != last_b) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          rope_cos_sin(w.r.p, 8 * (l16 & 7) + e, a.rope_pow, &cs[e], &sn[e]);
+        for (int e = 0; e < 4; ++e) rope_cos_sin(w.r.p, f[e], &cs[e], &sn[e]);
         last_b = w.b;
       }
       Seg<NG>& sg = segs[k % kSegs];
@@ -506,65 +507,65 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           !mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc))
         break;
       const bool owner = w.blk + w.len == w.r.n;
-      float kn[8];                                             // as the cache stores it
+      RowPart kn{};                                            // as the cache stores it
       if (owner) {                                             // every half-warp the same row
-        float y[8];
-        unpack8(cur.k, kn);
-        unpack8(cur.v, y);
+        kn = unpack_row(cur.k);
+        RowPart vn = unpack_row(cur.v);
         row_prologue(kn, wk, cs, sn, a.rope, a.eps);
-        uint4 kb, vb = cur.v;
+        RowBits kb, vb = cur.v;
         if constexpr (kF8) {
-          const uint2 bk = pack_e4m3_row(kn, cur.ks), bv = pack_e4m3_row(y, cur.vs);
-          kb = make_uint4(bk.x, bk.y, 0, 0);
-          vb = make_uint4(bv.x, bv.y, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            kn[e] = e4m3_to_f32(((e < 4 ? bk.x : bk.y) >> (8 * (e & 3))) & 0xff) * cur.ks;
-            y[e] = e4m3_to_f32(((e < 4 ? bv.x : bv.y) >> (8 * (e & 3))) & 0xff) * cur.vs;
-          }
+          kb = pack_e4m3(kn, 1.f / cur.ks);
+          vb = pack_e4m3(vn, 1.f / cur.vs);
+          kn = unpack_e4m3(kb, cur.ks);
+          vn = unpack_e4m3(vb, cur.vs);
         } else {
-          kb = pack_bf16_row(kn);
-          unpack8(kb, kn);
+          kb = pack_bf16(kn);
+          kn = unpack_row(kb);
         }
         if (hw == 0) {
           sg.kbits[l16] = kb;
           sg.vbits[l16] = vb;
-          *reinterpret_cast<float4*>(&sg.vnew[8 * l16]) = make_float4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<float4*>(&sg.vnew[8 * l16 + 4]) = make_float4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+          for (int h2 = 0; h2 < 2; ++h2)
+            *reinterpret_cast<float4*>(&sg.vnew[64 * h2 + 4 * l16]) =
+                make_float4(vn.x[h2][0], vn.x[h2][1], vn.x[h2][2], vn.x[h2][3]);
         }
       }
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = hw + kHw * i;
-        float x[8];
-        unpack8(cur.q[i], x);
+        RowPart x = unpack_row(cur.q[i]);
         row_prologue(x, wq, cs, sn, a.rope, a.eps);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = r < a.G ? x[e] * A.scale_log2 : 0.f;   // zero past G
+        for (int h2 = 0; h2 < 2; ++h2)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)                          // zero past G
+            x.x[h2][e] = r < a.G ? x.x[h2][e] * A.scale_log2 : 0.f;
         if (owner) {                                           // the new token's score
           float z = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) z += x[e] * kn[e];
+          for (int e = 0; e < 4; ++e) z += x.x[0][e] * kn.x[0][e] + x.x[1][e] * kn.x[1][e];
 #pragma unroll
           for (int o = 8; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
           if (l16 == 0) sg.snew[r] = z;
         }
-        uint32_t hi[4], lo[4];
+        // The lane's channels 4 l16 .. are a quarter of chunk l16 / 4 (and of chunk
+        // l16 / 4 + 4). bf16: the lanes of head r (4 r + tig) hold channels 2 tig,
+        // + 1 (x, y) and 2 tig + 8, + 9 (z, w) of a chunk. Over e4m3 a lane's four
+        // bytes are channels 4 tig .., so q takes them in that order as well.
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split_pair<kF8>(x[2 * e], x[2 * e + 1], hi[e], lo[e]);
-        // Channels 8 l16 .. are half of chunk l16 / 2. bf16: the lanes of head r
-        // (4 r + tig) hold channels 2 tig, + 1 and 2 tig + 8, + 9 of a chunk.
-        // Over e4m3 a lane's four bytes are channels 4 tig .., so q takes the
-        // chunk's channels in that order as well.
-        uint4* f = sg.frag + ((r >> 3) * 8 + (l16 >> 1)) * 32 + 4 * (r & 7);
-        if constexpr (kF8) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            f[2 * (l16 & 1) + e] = make_uint4(hi[2 * e], lo[2 * e], hi[2 * e + 1], lo[2 * e + 1]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            reinterpret_cast<uint2*>(f + e)[l16 & 1] = make_uint2(hi[e], lo[e]);
+        for (int h2 = 0; h2 < 2; ++h2) {
+          uint32_t hi0, lo0, hi1, lo1;
+          split_pair<kF8>(x.x[h2][0], x.x[h2][1], hi0, lo0);
+          split_pair<kF8>(x.x[h2][2], x.x[h2][3], hi1, lo1);
+          uint4* fr = sg.frag + ((r >> 3) * 8 + 4 * h2 + (l16 >> 2)) * 32 + 4 * (r & 7);
+          if constexpr (kF8) {
+            fr[l16 & 3] = make_uint4(hi0, lo0, hi1, lo1);
+          } else {
+            const int tig0 = 2 * (l16 & 1), zw = (l16 >> 1) & 1;
+            reinterpret_cast<uint2*>(fr + tig0)[zw] = make_uint2(hi0, lo0);
+            reinterpret_cast<uint2*>(fr + tig0 + 1)[zw] = make_uint2(hi1, lo1);
+          }
         }
       }
       if (lead && lane < 16) sg.sink[lane] = cur.sink;
@@ -838,8 +839,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     }
     if (owner && warp == kMathWarps - 1 && lane < 16 && !no_page) {
       const long long off = sg.dst + sg.g * a.c.head_stride;
-      store_bits(a.c, a.c.k, off, sg.kbits[lane]);
-      store_bits(a.c, a.c.v, off, sg.vbits[lane]);
+      store_row<kF8>(a.c.k, off, sg.kbits[lane]);
+      store_row<kF8>(a.c.v, off, sg.vbits[lane]);
     }
     if (no_page && threadIdx.x == 0) atomicOr(a.status, kStatusDecodeRange);
     if (!whole) {                                              // to be joined at the end

@@ -47,94 +47,125 @@ inline RopePowers rope_powers(double theta) {
   for (int i = 0; i < 6; ++i) r.pow[i] = std::exp2(-(double)(1 << i) / 64 * std::log2(theta));
   return r;
 }
-// cos and sin of pos * theta^(-2j/D). The angle is formed and reduced in double:
-// in float it would be off by 0.004 rad at position 131071. Taking it in turns
-// makes the reduction exact and lets sinpi / cospi do without their own (with
-// exp2 and sincosf here, a table of 64 angles took 5000 cycles).
-__device__ __forceinline__ void rope_cos_sin(int pos, int j, const RopePowers& w, float* c,
-                                             float* s) {
+__device__ __forceinline__ double rope_turns(int j, const RopePowers& w) {
   double f = 0.15915494309189533577;         // 1 / 2 pi
 #pragma unroll
   for (int i = 0; i < 6; ++i)
     if (j & (1 << i)) f *= w.pow[i];
+  return f;
+}
+// cos and sin of pos turns of 2 pi f. The angle is formed and reduced in double:
+// in float it would be off by 0.004 rad at position 131071. Taking it in turns
+// makes the reduction exact and lets sinpi / cospi do without their own (with
+// exp2 and sincosf here, a table of 64 angles took 5000 cycles).
+__device__ __forceinline__ void rope_cos_sin(int pos, double f, float* c, float* s) {
   double turns = (double)pos * f;
   turns -= rint(turns);
   sincospif(2.f * (float)turns, s, c);
 }
 
-__device__ __forceinline__ void unpack8(uint4 u, float (&f)[8]) {
-  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
+// A row of 128 channels belongs to a half-warp: lane l has channels 4l .. 4l+3 (x[0])
+// and 64 + 4l .. (x[1]), which RoPE rotates with each other, so the rotation stays
+// in the lane and takes four angles.
+struct RowPart {
+  float x[2][4];
+};
+// The lane's 8 bf16 of a row as they lie in memory; lo: channels 4l .., hi: 64 + 4l ..
+struct RowBits {
+  uint2 lo, hi;
+};
+__device__ __forceinline__ RowBits load_row(const __nv_bfloat16* row) {
+  const int l = threadIdx.x & 15;
+  return {*reinterpret_cast<const uint2*>(row + 4 * l),
+          *reinterpret_cast<const uint2*>(row + kHeadDim / 2 + 4 * l)};
+}
+__device__ __forceinline__ RowPart unpack_row(RowBits b) {
+  const uint32_t u[2][2] = {{b.lo.x, b.lo.y}, {b.hi.x, b.hi.y}};
+  RowPart r;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 t = __bfloat1622float2(h[i]);
-    f[2 * i] = t.x;
-    f[2 * i + 1] = t.y;
-  }
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      r.x[h][2 * i] = __uint_as_float(u[h][i] << 16);
+      r.x[h][2 * i + 1] = __uint_as_float(u[h][i] & 0xffff0000u);
+    }
+  return r;
 }
 
-// RMSNorm with weight w, then (rope) the rotation of channel j with j + 64. A
-// half-warp owns the row, lane l of it channels 8l .. 8l+7, whose partners are
-// in lane l ^ 8; cs, sn: the cosines and sines of the lane's channels (angles
-// 8 (l & 7) ..). The whole warp calls it (full-mask shuffles). The append and
-// the decode kernel use this one function, so both store the same bits for the
-// same token.
-__device__ __forceinline__ void row_prologue(float (&x)[8], const float (&w)[8], const float* cs,
-                                             const float* sn, bool rope, float eps) {
+// RMSNorm with weight w, then (rope) the rotation of channel j with j + 64 by the
+// lane's angles 4l .. 4l+3. The whole warp calls it (full-mask shuffles). The
+// append and the decode kernel use this one function, so both store the same
+// bits for the same token.
+__device__ __forceinline__ void row_prologue(RowPart& r, const RowPart& w, const float (&cs)[4],
+                                             const float (&sn)[4], bool rope, float eps) {
   float ss = 0.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
+  for (int e = 0; e < 4; ++e) ss += r.x[0][e] * r.x[0][e] + r.x[1][e] * r.x[1][e];
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float r = rsqrtf(ss * (1.0f / kHeadDim) + eps);
+  const float inv = rsqrtf(ss * (1.0f / kHeadDim) + eps);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = x[e] * r * w[e];
-  if (rope) {
-    const float sign = (threadIdx.x & 8) ? 1.f : -1.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float partner = __shfl_xor_sync(0xffffffffu, x[e], 8);
-      x[e] = x[e] * cs[e] + partner * (sign * sn[e]);
-    }
+  for (int e = 0; e < 4; ++e) {
+    const float a = r.x[0][e] * inv * w.x[0][e], b = r.x[1][e] * inv * w.x[1][e];
+    r.x[0][e] = rope ? a * cs[e] - b * sn[e] : a;
+    r.x[1][e] = rope ? b * cs[e] + a * sn[e] : b;
   }
 }
 
-// Eight values as the cache stores them: bf16 (16 bytes), or e4m3 of x / scale,
-// saturated to +-448 (8 bytes). One rounding each, to nearest even.
-__device__ __forceinline__ uint4 pack_bf16_row(const float (&x)[8]) {
-  uint4 u;
-  __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
+// The lane's part of a row as the cache stores it: bf16 (4 + 4 values), or e4m3 of
+// x * inv_scale, saturated to +-448 (lo.x and hi.x, 4 bytes each). One rounding
+// to nearest even; the product with the reciprocal is within 2^-23 of the quotient
+// (16 divisions a lane cost as much as the rest of the row).
+__device__ __forceinline__ RowBits pack_bf16(const RowPart& r) {
+  RowBits b;
+  uint32_t u[2][2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) h[i] = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
-  return u;
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const __nv_bfloat162 v = __floats2bfloat162_rn(r.x[h][2 * i], r.x[h][2 * i + 1]);
+      u[h][i] = *reinterpret_cast<const uint32_t*>(&v);
+    }
+  b.lo = make_uint2(u[0][0], u[0][1]);
+  b.hi = make_uint2(u[1][0], u[1][1]);
+  return b;
 }
-__device__ __forceinline__ uint2 pack_e4m3_row(const float (&x)[8], float scale) {
-  uint32_t h[4];
+__device__ __forceinline__ RowBits pack_e4m3(const RowPart& r, float inv_scale) {
+  uint32_t u[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    h[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] / scale, x[2 * i + 1] / scale),
-                                    __NV_SATFINITE, __NV_E4M3);
-  return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t a = __nv_cvt_float2_to_fp8x2(
+        make_float2(r.x[h][0] * inv_scale, r.x[h][1] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+    const uint32_t b = __nv_cvt_float2_to_fp8x2(
+        make_float2(r.x[h][2] * inv_scale, r.x[h][3] * inv_scale), __NV_SATFINITE, __NV_E4M3);
+    u[h] = a | (b << 16);
+  }
+  return {make_uint2(u[0], 0), make_uint2(u[1], 0)};
 }
 __device__ __forceinline__ float e4m3_to_f32(uint32_t bits) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)bits, __NV_E4M3)));
 }
-// Stores the lane's channels 8l .. 8l+7 of a row at element offset off (e4m3:
-// the first 8 bytes of u).
-__device__ __forceinline__ void store_bits(const PagedCache& c, void* pool, long long off,
-                                           uint4 u) {
-  const int l = threadIdx.x & 15;
-  if (c.e4m3)
-    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(pool) + off + 8 * l) = make_uint2(u.x, u.y);
-  else
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(pool) + off + 8 * l) = u;
+__device__ __forceinline__ RowPart unpack_e4m3(RowBits b, float scale) {
+  RowPart r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    r.x[0][e] = e4m3_to_f32((b.lo.x >> (8 * e)) & 0xff) * scale;
+    r.x[1][e] = e4m3_to_f32((b.hi.x >> (8 * e)) & 0xff) * scale;
+  }
+  return r;
 }
-__device__ __forceinline__ void store_row(const PagedCache& c, void* pool, long long off,
-                                          const float (&x)[8], float scale) {
-  if (c.e4m3) {
-    const uint2 u = pack_e4m3_row(x, scale);
-    store_bits(c, pool, off, make_uint4(u.x, u.y, 0, 0));
+// Stores the lane's part of a row at element offset off.
+template <bool kE4m3>
+__device__ __forceinline__ void store_row(void* pool, long long off, RowBits b) {
+  const int l = threadIdx.x & 15;
+  if constexpr (kE4m3) {
+    uint8_t* row = static_cast<uint8_t*>(pool) + off + 4 * l;
+    *reinterpret_cast<uint32_t*>(row) = b.lo.x;
+    *reinterpret_cast<uint32_t*>(row + kHeadDim / 2) = b.hi.x;
   } else {
-    store_bits(c, pool, off, pack_bf16_row(x));
+    __nv_bfloat16* row = static_cast<__nv_bfloat16*>(pool) + off + 4 * l;
+    *reinterpret_cast<uint2*>(row) = b.lo;
+    *reinterpret_cast<uint2*>(row + kHeadDim / 2) = b.hi;
   }
 }
 
@@ -149,7 +180,7 @@ struct PagedAppendLaunch {
   const int32_t *cu, *lens;
   int* status;
 };
-cudaError_t launch_paged_append(const PagedAppendLaunch& a, cudaStream_t st);
+cudaError_t launch_paged_append(const PagedAppendLaunch& a, int num_sms, cudaStream_t st);
 
 struct PagedDecodeLaunch {
   PagedCache c;

@@ -7,80 +7,97 @@
 // layers, FlintAttention: per-head RMSNorm, then RoPE on selected layers).
 //
 // Bound by HBM: 512 bytes of K and V read per (token, KV head) and 512 (bf16)
-// or 256 (e4m3) written, against ~100 operations. A block takes kTok tokens;
-// it finds their slots and builds their cos/sin table once for all heads, then
-// each half-warp moves one head's K and V row at a time with 16-byte accesses.
+// or 256 (e4m3) written, against ~100 operations. A half-warp takes a token: it
+// requests the rows of up to kHeads heads, then finds the token's slot and its 64
+// angles (four a lane, shared by all heads) while they come, and needs neither
+// shared memory nor a barrier. Blocks are persistent, so a lane forms its four
+// frequencies once.
 #include "paged.cuh"
 
 namespace flint {
 
 namespace {
 
-constexpr int kTok = 4;
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;                // 8 tokens at a time
+constexpr int kHeads = 4;                    // heads in flight: 16 loads of 8 bytes a lane
+constexpr int kBlocks = 5;                   // per SM
 
-__global__ void __launch_bounds__(kThreads) paged_append_kernel(const PagedAppendLaunch a) {
-  __shared__ float cs[kTok][kHeadDim / 2], sn[kTok][kHeadDim / 2];
-  __shared__ long long slot[kTok];     // element offset of the token's slot, -1: none
-  __shared__ int pos_s[kTok];
-  const int t0 = blockIdx.x * kTok;
-  if (threadIdx.x < kTok) {
-    const int t = t0 + threadIdx.x;
-    long long off = -1;
-    int pos = 0;
-    if (t < a.T && t < __ldg(a.cu + a.N)) {          // tokens past the last sequence: none
-      const int b = doc_of(a.cu, a.N, t);
-      const int len = __ldg(a.lens + b);
-      const long long p = (long long)len + t - __ldg(a.cu + b);
-      if (len != -1) {                               // -1: a row that is not in use
-        if (len >= 0 && p >= 0 && p < (long long)a.c.P * a.c.max_pages) {
-          pos = (int)p;
-          off = slot_offset(a.c, b, pos);
+template <bool kE4m3>
+__global__ void __launch_bounds__(kThreads, kBlocks)
+paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
+  const int l = threadIdx.x & 15;
+  const RowPart w = unpack_row(load_row(a.wk));
+  double f[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) f[e] = rope_turns(4 * l + e, a.rope_pow);
+  const int used = min(a.T, __ldg(a.cu + a.N));      // tokens past the last sequence: none
+  const long long step = (long long)gridDim.x * (kThreads / 16);
+  const long long first = (long long)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
+  // Both half-warps of a warp take as many turns: the shuffles are the warp's.
+  for (long long t0 = first - (threadIdx.x >> 4 & 1); t0 < used; t0 += step) {
+    const long long t = t0 + (threadIdx.x >> 4 & 1);
+    const bool live = t < used;
+    const __nv_bfloat16* krow = a.k + (live ? t : t0) * a.k_stride;
+    const __nv_bfloat16* vrow = a.v + (live ? t : t0) * a.v_stride;
+    RowBits kb[kHeads], vb[kHeads];
+    auto request = [&](int g0) {
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i)
+        if (g0 + i < a.c.Hk) {
+          kb[i] = load_row(krow + (g0 + i) * kHeadDim);
+          vb[i] = load_row(vrow + (g0 + i) * kHeadDim);
         }
-        if (off < 0) atomicOr(a.status, kStatusDecodeRange);
+    };
+    request(0);
+    long long off = -1;                              // the token's slot, -1: none
+    int pos = 0;
+    if (live) {
+      const int b = doc_of(a.cu, a.N, (int)t), len = __ldg(a.lens + b);
+      const long long p = len + t - __ldg(a.cu + b);
+      if (len >= 0 && p >= 0 && p < (long long)a.c.P * a.c.max_pages) {
+        pos = (int)p;
+        off = slot_offset(a.c, b, pos);
       }
+      // -1 marks a sequence that is not in use
+      if (off < 0 && len != -1 && l == 0) atomicOr(a.status, kStatusDecodeRange);
     }
-    slot[threadIdx.x] = off;
-    pos_s[threadIdx.x] = pos;
-  }
-  __syncthreads();
-  if (a.rope) {
-    for (int e = threadIdx.x; e < kTok * (kHeadDim / 2); e += kThreads) {
-      const int i = e / (kHeadDim / 2), j = e % (kHeadDim / 2);
-      rope_cos_sin(pos_s[i], j, a.rope_pow, &cs[i][j], &sn[i][j]);
-    }
-    __syncthreads();
-  }
-  const int l = threadIdx.x & 15, grp = threadIdx.x >> 4;
-  float w[8];
-  load8(a.wk + 8 * l, w);
-  const int rows = kTok * a.c.Hk;
-  const int iters = (rows + kThreads / 16 - 1) / (kThreads / 16);   // whole warps in every one
-  for (int it = 0; it < iters; ++it) {
-    const int rr = grp + it * (kThreads / 16);
-    const int i = rr < rows ? rr / a.c.Hk : 0, g = rr % a.c.Hk;
-    const bool live = rr < rows && slot[i] >= 0;
-    float x[8] = {}, y[8] = {};
-    if (live) {
-      const long long t = t0 + i;
-      load8(a.k + t * a.k_stride + g * kHeadDim + 8 * l, x);
-      load8(a.v + t * a.v_stride + g * kHeadDim + 8 * l, y);
-    }
-    row_prologue(x, w, &cs[i][8 * (l & 7)], &sn[i][8 * (l & 7)], a.rope, a.eps);
-    if (live) {
-      const long long off = slot[i] + g * a.c.head_stride;
-      store_row(a.c, a.c.k, off, x, a.c.k_scale ? __ldg(a.c.k_scale + g) : 1.f);
-      store_row(a.c, a.c.v, off, y, a.c.v_scale ? __ldg(a.c.v_scale + g) : 1.f);
+    float cs[4], sn[4];
+    if (a.rope)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rope_cos_sin(pos, f[e], &cs[e], &sn[e]);
+    for (int g0 = 0; g0 < a.c.Hk; g0 += kHeads) {
+      if (g0) request(g0);
+#pragma unroll
+      for (int i = 0; i < kHeads; ++i) {
+        const int g = g0 + i;
+        if (g >= a.c.Hk) break;
+        RowPart x = unpack_row(kb[i]);
+        row_prologue(x, w, cs, sn, a.rope, a.eps);
+        RowBits ko, vo = vb[i];
+        if constexpr (kE4m3) {
+          ko = pack_e4m3(x, 1.f / (a.c.k_scale ? __ldg(a.c.k_scale + g) : 1.f));
+          vo = pack_e4m3(unpack_row(vo), 1.f / (a.c.v_scale ? __ldg(a.c.v_scale + g) : 1.f));
+        } else {
+          ko = pack_bf16(x);
+        }
+        if (off >= 0) {
+          store_row<kE4m3>(a.c.k, off + g * a.c.head_stride, ko);
+          store_row<kE4m3>(a.c.v, off + g * a.c.head_stride, vo);
+        }
+      }
     }
   }
 }
 
 }  // namespace
 
-cudaError_t launch_paged_append(const PagedAppendLaunch& a, cudaStream_t st) {
+cudaError_t launch_paged_append(const PagedAppendLaunch& a, int num_sms, cudaStream_t st) {
   ProfScope prof(kKPagedAppend, st);
-  const unsigned grid = ((unsigned)a.T + kTok - 1) / kTok;
-  paged_append_kernel<<<grid, kThreads, 0, st>>>(a);
+  const int per = kThreads / 16;
+  const int blocks = (int)(((long long)a.T + per - 1) / per);
+  const int grid = blocks < kBlocks * num_sms ? blocks : kBlocks * num_sms;
+  if (a.c.e4m3) paged_append_kernel<true><<<grid, kThreads, 0, st>>>(a);
+  else paged_append_kernel<false><<<grid, kThreads, 0, st>>>(a);
   return cudaGetLastError();
 }
 
