@@ -466,7 +466,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     constexpr int kHw = 2 * kRowWarps, kRows = 8 * NG / kHw;   // rows of a half-warp: hw + kHw i
     const bool lead = warp == kMathWarps;
     const RowPart wq = unpack_row(load_row(a.wq)), wk = unpack_row(load_row(a.wk));
-    float cs[4], sn[4];
+    Angles angles{};
     double f[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) f[e] = rope_turns(4 * l16 + e, a.rope_pow);
@@ -497,11 +497,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool more = nx.next(a, sm.lens);
       const Raw cur = h;
       if (more) h = look(nx);
-      if (a.rope && w.b != last_b) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) rope_cos_sin(w.r.p, f[e], &cs[e], &sn[e]);
-        last_b = w.b;
-      }
+      if (a.rope && w.b != last_b) angles = row_angles(w.r.p, f);
+      last_b = w.b;
       Seg<NG>& sg = segs[k % kSegs];
       if (k >= kSegs &&
           !mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc))
@@ -511,11 +508,11 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (owner) {                                             // every half-warp the same row
         kn = unpack_row(cur.k);
         RowPart vn = unpack_row(cur.v);
-        row_prologue(kn, wk, cs, sn, a.rope, a.eps);
+        row_prologue(kn, wk, angles, a.rope, a.eps);
         RowBits kb, vb = cur.v;
         if constexpr (kF8) {
-          kb = pack_e4m3(kn, 1.f / cur.ks);
-          vb = pack_e4m3(vn, 1.f / cur.vs);
+          kb = pack_e4m3(kn, inv_scale(a.c.k_scale, w.g));
+          vb = pack_e4m3(vn, inv_scale(a.c.v_scale, w.g));
           kn = unpack_e4m3(kb, cur.ks);
           vn = unpack_e4m3(vb, cur.vs);
         } else {
@@ -527,24 +524,28 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           sg.vbits[l16] = vb;
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2)
-            *reinterpret_cast<float4*>(&sg.vnew[64 * h2 + 4 * l16]) =
-                make_float4(vn.x[h2][0], vn.x[h2][1], vn.x[h2][2], vn.x[h2][3]);
+            *reinterpret_cast<ulonglong2*>(&sg.vnew[64 * h2 + 4 * l16]) =
+                make_ulonglong2(vn.x[h2][0], vn.x[h2][1]);
         }
       }
 #pragma unroll
       for (int i = 0; i < kRows; ++i) {
         const int r = hw + kHw * i;
         RowPart x = unpack_row(cur.q[i]);
-        row_prologue(x, wq, cs, sn, a.rope, a.eps);
+        row_prologue(x, wq, angles, a.rope, a.eps);
+        float z = 0.f, xs[2][4];
 #pragma unroll
-        for (int h2 = 0; h2 < 2; ++h2)
+        for (int h2 = 0; h2 < 2; ++h2) {
+          float kh[4];
+          x.get(h2, xs[h2]);
+          kn.get(h2, kh);
 #pragma unroll
-          for (int e = 0; e < 4; ++e)                          // zero past G
-            x.x[h2][e] = r < a.G ? x.x[h2][e] * A.scale_log2 : 0.f;
+          for (int e = 0; e < 4; ++e) {
+            xs[h2][e] = r < a.G ? xs[h2][e] * A.scale_log2 : 0.f;   // zero past G
+            z += xs[h2][e] * kh[e];
+          }
+        }
         if (owner) {                                           // the new token's score
-          float z = 0.f;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) z += x.x[0][e] * kn.x[0][e] + x.x[1][e] * kn.x[1][e];
 #pragma unroll
           for (int o = 8; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
           if (l16 == 0) sg.snew[r] = z;
@@ -556,8 +557,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
 #pragma unroll
         for (int h2 = 0; h2 < 2; ++h2) {
           uint32_t hi0, lo0, hi1, lo1;
-          split_pair<kF8>(x.x[h2][0], x.x[h2][1], hi0, lo0);
-          split_pair<kF8>(x.x[h2][2], x.x[h2][3], hi1, lo1);
+          split_pair<kF8>(xs[h2][0], xs[h2][1], hi0, lo0);
+          split_pair<kF8>(xs[h2][2], xs[h2][3], hi1, lo1);
           uint4* fr = sg.frag + ((r >> 3) * 8 + 4 * h2 + (l16 >> 2)) * 32 + 4 * (r & 7);
           if constexpr (kF8) {
             fr[l16 & 3] = make_uint4(hi0, lo0, hi1, lo1);

@@ -13,6 +13,7 @@
 #include <cuda_fp8.h>
 
 #include "common.cuh"
+#include "sm100_primitives.cuh"
 
 namespace flint {
 
@@ -66,9 +67,17 @@ __device__ __forceinline__ void rope_cos_sin(int pos, double f, float* c, float*
 
 // A row of 128 channels belongs to a half-warp: lane l has channels 4l .. 4l+3 (x[0])
 // and 64 + 4l .. (x[1]), which RoPE rotates with each other, so the rotation stays
-// in the lane and takes four angles.
+// in the lane and takes four angles. Two channels to a register pair, so that the
+// packed FP32 instructions do a row in half as many.
 struct RowPart {
-  float x[2][4];
+  uint64_t x[2][2];
+  __device__ __forceinline__ void get(int h, float (&f)[4]) const {
+    f2_split(x[h][0], f[0], f[1]);
+    f2_split(x[h][1], f[2], f[3]);
+  }
+};
+struct Angles {
+  uint64_t c[2], s[2], minus_s[2];           // of channels 4l .. 4l+3
 };
 // The lane's 8 bf16 of a row as they lie in memory; lo: channels 4l .., hi: 64 + 4l ..
 struct RowBits {
@@ -79,68 +88,80 @@ __device__ __forceinline__ RowBits load_row(const __nv_bfloat16* row) {
   return {*reinterpret_cast<const uint2*>(row + 4 * l),
           *reinterpret_cast<const uint2*>(row + kHeadDim / 2 + 4 * l)};
 }
+__device__ __forceinline__ uint64_t bf16x2_to_f2(uint32_t u) {
+  return f2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
 __device__ __forceinline__ RowPart unpack_row(RowBits b) {
-  const uint32_t u[2][2] = {{b.lo.x, b.lo.y}, {b.hi.x, b.hi.y}};
-  RowPart r;
+  return {{{bf16x2_to_f2(b.lo.x), bf16x2_to_f2(b.lo.y)},
+           {bf16x2_to_f2(b.hi.x), bf16x2_to_f2(b.hi.y)}}};
+}
+// The row's four angles at pos; f: the lane's frequencies in turns.
+__device__ __forceinline__ Angles row_angles(int pos, const double (&f)[4]) {
+  float c[4], s[4];
 #pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      r.x[h][2 * i] = __uint_as_float(u[h][i] << 16);
-      r.x[h][2 * i + 1] = __uint_as_float(u[h][i] & 0xffff0000u);
-    }
-  return r;
+  for (int e = 0; e < 4; ++e) rope_cos_sin(pos, f[e], &c[e], &s[e]);
+  return {{f2(c[0], c[1]), f2(c[2], c[3])},
+          {f2(s[0], s[1]), f2(s[2], s[3])},
+          {f2(-s[0], -s[1]), f2(-s[2], -s[3])}};
 }
 
 // RMSNorm with weight w, then (rope) the rotation of channel j with j + 64 by the
-// lane's angles 4l .. 4l+3. The whole warp calls it (full-mask shuffles). The
-// append and the decode kernel use this one function, so both store the same
-// bits for the same token.
-__device__ __forceinline__ void row_prologue(RowPart& r, const RowPart& w, const float (&cs)[4],
-                                             const float (&sn)[4], bool rope, float eps) {
-  float ss = 0.f;
-#pragma unroll
-  for (int e = 0; e < 4; ++e) ss += r.x[0][e] * r.x[0][e] + r.x[1][e] * r.x[1][e];
+// lane's angles. The whole warp calls it (full-mask shuffles). The append and the
+// decode kernel use this one function, so both store the same bits for the same
+// token.
+__device__ __forceinline__ void row_prologue(RowPart& r, const RowPart& w, const Angles& t,
+                                             bool rope, float eps) {
+  const uint64_t q = ffma2(r.x[0][0], r.x[0][0], fmul2(r.x[0][1], r.x[0][1]));
+  float s0, s1;
+  f2_split(ffma2(r.x[1][0], r.x[1][0], ffma2(r.x[1][1], r.x[1][1], q)), s0, s1);
+  float ss = s0 + s1;
 #pragma unroll
   for (int o = 8; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
   const float inv = rsqrtf(ss * (1.0f / kHeadDim) + eps);
+  const uint64_t inv2 = f2(inv, inv);
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float a = r.x[0][e] * inv * w.x[0][e], b = r.x[1][e] * inv * w.x[1][e];
-    r.x[0][e] = rope ? a * cs[e] - b * sn[e] : a;
-    r.x[1][e] = rope ? b * cs[e] + a * sn[e] : b;
+  for (int i = 0; i < 2; ++i) {
+    const uint64_t a = fmul2(fmul2(r.x[0][i], inv2), w.x[0][i]);
+    const uint64_t b = fmul2(fmul2(r.x[1][i], inv2), w.x[1][i]);
+    r.x[0][i] = rope ? ffma2(b, t.minus_s[i], fmul2(a, t.c[i])) : a;
+    r.x[1][i] = rope ? ffma2(a, t.s[i], fmul2(b, t.c[i])) : b;
   }
 }
 
 // The lane's part of a row as the cache stores it: bf16 (4 + 4 values), or e4m3 of
 // x * inv_scale, saturated to +-448 (lo.x and hi.x, 4 bytes each). One rounding
-// to nearest even; the product with the reciprocal is within 2^-23 of the quotient
+// to nearest even; the product with the reciprocal is within 2^-22 of the quotient
 // (16 divisions a lane cost as much as the rest of the row).
-__device__ __forceinline__ RowBits pack_bf16(const RowPart& r) {
-  RowBits b;
-  uint32_t u[2][2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const __nv_bfloat162 v = __floats2bfloat162_rn(r.x[h][2 * i], r.x[h][2 * i + 1]);
-      u[h][i] = *reinterpret_cast<const uint32_t*>(&v);
-    }
-  b.lo = make_uint2(u[0][0], u[0][1]);
-  b.hi = make_uint2(u[1][0], u[1][1]);
-  return b;
+__device__ __forceinline__ float inv_scale(const float* scale, int g) {
+  float r = 1.f;
+  if (scale) asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(__ldg(scale + g)));
+  return r;
 }
-__device__ __forceinline__ RowBits pack_e4m3(const RowPart& r, float inv_scale) {
-  uint32_t u[2];
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const uint32_t a = __nv_cvt_float2_to_fp8x2(
-        make_float2(r.x[h][0] * inv_scale, r.x[h][1] * inv_scale), __NV_SATFINITE, __NV_E4M3);
-    const uint32_t b = __nv_cvt_float2_to_fp8x2(
-        make_float2(r.x[h][2] * inv_scale, r.x[h][3] * inv_scale), __NV_SATFINITE, __NV_E4M3);
-    u[h] = a | (b << 16);
-  }
-  return {make_uint2(u[0], 0), make_uint2(u[1], 0)};
+__device__ __forceinline__ uint32_t f2_to_bf16x2(uint64_t v) {
+  float a, b;
+  f2_split(v, a, b);
+  return pack_bf16x2(a, b);
+}
+__device__ __forceinline__ RowBits pack_bf16(const RowPart& r) {
+  return {make_uint2(f2_to_bf16x2(r.x[0][0]), f2_to_bf16x2(r.x[0][1])),
+          make_uint2(f2_to_bf16x2(r.x[1][0]), f2_to_bf16x2(r.x[1][1]))};
+}
+__device__ __forceinline__ uint32_t f2x2_to_e4m3(uint64_t u, uint64_t v) {
+  float a, b, c, d;
+  f2_split(u, a, b);
+  f2_split(v, c, d);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r) : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
+}
+__device__ __forceinline__ RowBits pack_e4m3(const RowPart& r, float inv) {
+  const uint64_t i2 = f2(inv, inv);
+  return {make_uint2(f2x2_to_e4m3(fmul2(r.x[0][0], i2), fmul2(r.x[0][1], i2)), 0),
+          make_uint2(f2x2_to_e4m3(fmul2(r.x[1][0], i2), fmul2(r.x[1][1], i2)), 0)};
 }
 __device__ __forceinline__ float e4m3_to_f32(uint32_t bits) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)bits, __NV_E4M3)));
@@ -148,10 +169,12 @@ __device__ __forceinline__ float e4m3_to_f32(uint32_t bits) {
 __device__ __forceinline__ RowPart unpack_e4m3(RowBits b, float scale) {
   RowPart r;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    r.x[0][e] = e4m3_to_f32((b.lo.x >> (8 * e)) & 0xff) * scale;
-    r.x[1][e] = e4m3_to_f32((b.hi.x >> (8 * e)) & 0xff) * scale;
-  }
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const uint32_t u = (h ? b.hi.x : b.lo.x) >> (16 * i);
+      r.x[h][i] = f2(e4m3_to_f32(u & 0xff) * scale, e4m3_to_f32((u >> 8) & 0xff) * scale);
+    }
   return r;
 }
 // Stores the lane's part of a row at element offset off.

@@ -61,10 +61,8 @@ paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
       // -1 marks a sequence that is not in use
       if (off < 0 && len != -1 && l == 0) atomicOr(a.status, kStatusDecodeRange);
     }
-    float cs[4], sn[4];
-    if (a.rope)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) rope_cos_sin(pos, f[e], &cs[e], &sn[e]);
+    Angles angles{};
+    if (a.rope) angles = row_angles(pos, f);
     for (int g0 = 0; g0 < a.c.Hk; g0 += kHeads) {
       if (g0) request(g0);
 #pragma unroll
@@ -72,11 +70,11 @@ paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
         const int g = g0 + i;
         if (g >= a.c.Hk) break;
         RowPart x = unpack_row(kb[i]);
-        row_prologue(x, w, cs, sn, a.rope, a.eps);
+        row_prologue(x, w, angles, a.rope, a.eps);
         RowBits ko, vo = vb[i];
         if constexpr (kE4m3) {
-          ko = pack_e4m3(x, 1.f / (a.c.k_scale ? __ldg(a.c.k_scale + g) : 1.f));
-          vo = pack_e4m3(unpack_row(vo), 1.f / (a.c.v_scale ? __ldg(a.c.v_scale + g) : 1.f));
+          ko = pack_e4m3(x, inv_scale(a.c.k_scale, g));
+          vo = pack_e4m3(unpack_row(vo), inv_scale(a.c.v_scale, g));
         } else {
           ko = pack_bf16(x);
         }
