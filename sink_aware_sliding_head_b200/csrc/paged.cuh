@@ -45,7 +45,8 @@ struct RopePowers {
 };
 inline RopePowers rope_powers(double theta) {
   RopePowers r;
-  for (int i = 0; i < 6; ++i) r.pow[i] = std::exp2(-(double)(1 << i) / 64 * std::log2(theta));
+  const double step = -std::log2(theta) / 64;
+  for (int i = 0; i < 6; ++i) r.pow[i] = std::exp2(step * (1 << i));
   return r;
 }
 __device__ __forceinline__ double rope_turns(int j, const RopePowers& w) {

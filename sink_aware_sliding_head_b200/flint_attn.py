@@ -436,86 +436,103 @@ def decode(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, k_cache, v_cache, wind
 # A pool may be head-major [pages, Hk, P, D] or any strided view of that shape
 # (a token-major pool transposed, one half of an interleaved K/V pool).
 
-def _on_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+# (A call's checks run on the host every time: they are written to take as few
+# tensor attributes as they can.)
+
+def _same_device(index, names, tensors):
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            where = ", ".join(f"{n} on {x.device}" for n, x in zip(names.split(), tensors)
+                              if x is not None)
+            raise ValueError(f"the tensors must be on one CUDA device: {where}")
 
 
 def _vector(t, name, dtype, shape):
-    if t is not None and (t.dtype != dtype or t.shape != shape or not t.is_contiguous()):
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {list(shape)}, got {t.dtype} "
                          f"{list(t.shape)}")
 
 
-def _rows(t, name, heads, D, n=None):
-    """Row stride of a bf16 [rows, heads, D] tensor whose rows are contiguous."""
-    if t.dtype != torch.bfloat16:
+def _rows(t, name, n, heads, D):
+    """Row stride of a bf16 [n, heads, D] tensor whose rows are contiguous."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[1:] != (heads, D) or (n is not None and t.shape[0] != n):
-        raise ValueError(f"{name} must be [{'rows' if n is None else n}, {heads}, {D}], got "
-                         f"{list(t.shape)}")
-    if (t.stride(2) != 1 and D > 1) or (t.stride(1) != D and heads > 1):
+    if t.shape != (n, heads, D):
+        raise ValueError(f"{name} must be [{n}, {heads}, {D}], got {list(t.shape)}")
+    row, head, channel = t.stride()
+    if (channel != 1 and D > 1) or (head != D and heads > 1):
         raise ValueError(f"{name}: the heads of a row must be contiguous, got strides {t.stride()}")
-    if t.shape[0] <= 1:
+    if n <= 1:
         return 0
-    if t.stride(0) < heads * D:                 # 0 would mean "contiguous" to the library
+    if row < heads * D:                          # 0 would mean "contiguous" to the library
         raise ValueError(f"{name}: rows must not overlap, got strides {t.stride()}")
-    return t.stride(0)
+    return row
+
+
+def _pool_strides(t):
+    # the stride of an axis of length 1 is never used and may be anything
+    D = t.shape[3]
+    return tuple(D if n == 1 else st for n, st in zip(t.shape[:3], t.stride())) + t.stride()[3:]
 
 
 def _paged_cache(k_pages, v_pages, block_table, rows, k_scale, v_scale) -> PagedCacheDesc:
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.dtype != v_pages.dtype:
+    shape, dtype = k_pages.shape, k_pages.dtype
+    if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dtype:
         raise ValueError("k_pages and v_pages must be [pages, Hk, page_size, D] of one type, got "
                          f"{k_pages.dtype} {list(k_pages.shape)} and {v_pages.dtype} "
                          f"{list(v_pages.shape)}")
-    if k_pages.dtype == torch.bfloat16:
+    n, Hk, P, D = shape
+    if dtype is torch.bfloat16:
         code = CACHE_BF16
         if k_scale is not None or v_scale is not None:
             raise ValueError("k_scale and v_scale belong to float8_e4m3fn caches")
-    elif k_pages.dtype == torch.float8_e4m3fn:
+    elif dtype is torch.float8_e4m3fn:
         code = CACHE_E4M3
+        for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+            if t is not None:
+                _vector(t, name, torch.float32, (Hk,))
     else:
-        raise TypeError(f"unsupported cache dtype {k_pages.dtype}")
-    n, Hk, P, D = k_pages.shape
-    # the stride of an axis of length 1 is never used and may be anything
-    strides, other = ([D if t.shape[i] == 1 else t.stride(i) for i in range(3)]
-                      for t in (k_pages, v_pages))
-    if strides != other:
-        raise ValueError(f"k_pages and v_pages have different strides: {k_pages.stride()} and "
-                         f"{v_pages.stride()}")
-    if min(strides) < D or k_pages.stride(3) != 1 or v_pages.stride(3) != 1:
+        raise TypeError(f"unsupported cache dtype {dtype}")
+    strides = k_pages.stride()
+    if strides != v_pages.stride() or n == 1 or Hk == 1 or P == 1:
+        strides = _pool_strides(k_pages)
+        if strides != _pool_strides(v_pages):
+            raise ValueError(f"k_pages and v_pages have different strides: {k_pages.stride()} and "
+                             f"{v_pages.stride()}")
+    page, head, slot, channel = strides
+    if page < D or head < D or slot < D or channel != 1:
         raise ValueError(f"slots must be {D} contiguous channels and not overlap, got strides "
                          f"{k_pages.stride()}")
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.shape[0] != rows \
-            or (block_table.shape[1] > 1 and block_table.stride(1) != 1) \
-            or (rows > 1 and block_table.stride(0) < block_table.shape[1]):
-        raise ValueError(f"block_table must be int32 [{rows}, max_pages] with contiguous rows, got "
-                         f"{block_table.dtype} {list(block_table.shape)}")
-    _vector(k_scale, "k_scale", torch.float32, (Hk,))
-    _vector(v_scale, "v_scale", torch.float32, (Hk,))
-    return PagedCacheDesc(n, P, block_table.shape[1], Hk, D, code, strides[0], strides[1],
-                          strides[2], block_table.stride(0) if rows > 1 else 0)
+    shape = block_table.shape
+    if len(shape) != 2 or shape[0] != rows or block_table.dtype is not torch.int32:
+        raise ValueError(f"block_table must be int32 [{rows}, max_pages], got {block_table.dtype} "
+                         f"{list(shape)}")
+    cols = shape[1]
+    row, col = block_table.stride()
+    if (col != 1 and cols > 1) or (row < cols and rows > 1):
+        raise ValueError("block_table: the entries of a row must be contiguous and rows not "
+                         f"overlap, got strides {block_table.stride()}")
+    return PagedCacheDesc(n, P, cols, Hk, D, code, page, head, slot, row if rows > 1 else 0)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _paged_call(device, stream, fn):
+def _paged_call(index, stream, fn):
     """Runs ``fn(stream handle)`` with the tensors' device current and, for a given
     stream, that stream current too, so that what fn allocates belongs to it."""
-    if device.type != "cuda":
-        raise ValueError(f"CUDA tensors expected, got {device}")
+    if index < 0:
+        raise ValueError("CUDA tensors expected")
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        if stream.device_index != index:
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
         with torch.cuda.stream(stream):
             return fn(stream.cuda_stream)
-    if device.index != torch.cuda.current_device():
-        with torch.cuda.device(device):
+    if index != torch.cuda.current_device():
+        with torch.cuda.device(index):
             return fn(torch.cuda.current_stream().cuda_stream)
-    return fn(torch.cuda.current_stream().cuda_stream)
+    return fn(torch.cuda.current_stream(index).cuda_stream)
 
 
 def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, v_pages, use_rope,
@@ -534,32 +551,35 @@ def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, 
     omitted); ``check_status`` synchronises and raises ``FlintError`` for them.
     """
     lib = load_library()
-    N = cache_lens.numel()
+    N, T = cache_lens.numel(), k.shape[0]
     desc = _paged_cache(k_pages, v_pages, block_table, N, k_scale, v_scale)
     Hk, D = desc.num_kv_heads, desc.head_dim
-    k_stride, v_stride = _rows(k, "k", Hk, D), _rows(v, "v", Hk, D, k.shape[0])
+    k_stride, v_stride = _rows(k, "k", T, Hk, D), _rows(v, "v", T, Hk, D)
     _vector(k_norm_w, "k_norm_w", torch.bfloat16, (D,))
     _vector(cache_lens, "cache_lens", torch.int32, (N,))
     _vector(cu_new_lens, "cu_new_lens", torch.int32, (N + 1,))
-    _vector(status, "status", torch.int32, (64,))
-    dev = k_pages.device
-    _on_device(dev, k=k, v=v, v_pages=v_pages, k_norm_w=k_norm_w, cu_new_lens=cu_new_lens,
-               cache_lens=cache_lens, block_table=block_table, k_scale=k_scale, v_scale=v_scale,
-               status=status)
-    p = PagedAppendParams(desc, N, k.shape[0], 1 if use_rope else 0, rope_theta, rms_eps,
-                          FLINT_BF16, k_stride, v_stride)
+    if status is not None:
+        _vector(status, "status", torch.int32, (64,))
+    index = k_pages.get_device()
+    _same_device(index, "k v k_norm_w cu_new_lens cache_lens block_table k_pages v_pages k_scale "
+                 "v_scale status", (k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages,
+                                    v_pages, k_scale, v_scale, status))
+    p = PagedAppendParams(desc, N, T, 1 if use_rope else 0, rope_theta, rms_eps, FLINT_BF16,
+                          k_stride, v_stride)
 
     def call(st):
-        word = torch.zeros(64, dtype=torch.int32, device=dev) if status is None else status
-        _check(lib.flint_attn_paged_append(
-            ctypes.byref(p), _addr(k), _addr(v), _addr(k_norm_w), _addr(cu_new_lens),
-            _addr(cache_lens), _addr(block_table), _addr(k_pages), _addr(v_pages),
-            _addr(k_scale), _addr(v_scale), _addr(word), st), "flint_attn_paged_append")
+        word = torch.zeros(64, dtype=torch.int32, device=k_pages.device) if status is None else status
+        code = lib.flint_attn_paged_append(
+            p, k.data_ptr(), v.data_ptr(), k_norm_w.data_ptr(), cu_new_lens.data_ptr(),
+            cache_lens.data_ptr(), block_table.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+            _addr(k_scale), _addr(v_scale), word.data_ptr(), st)
+        if code:
+            raise FlintError(code, "flint_attn_paged_append")
         if check_status:
-            _check(lib.flint_attn_check_status(_addr(word), st),
+            _check(lib.flint_attn_check_status(word.data_ptr(), st),
                    "flint_attn_paged_append (device)")
 
-    _paged_call(dev, stream, call)
+    _paged_call(index, stream, call)
 
 
 def alloc_decode_paged_workspace(batch, num_q_heads, num_kv_heads, device=None) -> torch.Tensor:
@@ -594,38 +614,44 @@ def decode_paged(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_p
     B = cache_lens.numel()
     desc = _paged_cache(k_pages, v_pages, block_table, B, k_scale, v_scale)
     Hk, D = desc.num_kv_heads, desc.head_dim
-    H = q.shape[1] if q.dim() == 3 else 0
-    strides = _rows(q, "q", H, D, B), _rows(k, "k", Hk, D, B), _rows(v, "v", Hk, D, B)
+    H = sink.numel()
+    p = DecodePagedParams(desc, B, H, window, 1 if use_rope else 0, rope_theta, rms_eps,
+                          softmax_scale, FLINT_BF16, 1 if fp32_out else 0, 0,
+                          _rows(q, "q", B, H, D), _rows(k, "k", B, Hk, D), _rows(v, "v", B, Hk, D))
     _vector(q_norm_w, "q_norm_w", torch.bfloat16, (D,))
     _vector(k_norm_w, "k_norm_w", torch.bfloat16, (D,))
     _vector(sink, "sink", torch.float32, (H,))
     _vector(cache_lens, "cache_lens", torch.int32, (B,))
     odt = torch.float32 if fp32_out else torch.bfloat16
-    _vector(out, "out", odt, (B, H, D))
-    _vector(lse, "lse", torch.float32, (B, H))
+    if out is not None:
+        _vector(out, "out", odt, (B, H, D))
+    if lse is not None:
+        _vector(lse, "lse", torch.float32, (B, H))
     if workspace is not None:
         _vector(workspace, "workspace", torch.uint8, (workspace.numel(),))
-    dev = k_pages.device
-    _on_device(dev, q=q, k=k, v=v, v_pages=v_pages, q_norm_w=q_norm_w, k_norm_w=k_norm_w,
-               sink=sink, cache_lens=cache_lens, block_table=block_table, k_scale=k_scale,
-               v_scale=v_scale, out=out, lse=lse, workspace=workspace)
-    p = DecodePagedParams(desc, B, H, window, 1 if use_rope else 0, rope_theta, rms_eps,
-                          softmax_scale, FLINT_BF16, 1 if fp32_out else 0, 0, *strides)
+    index = k_pages.get_device()
+    _same_device(index, "q k v q_norm_w k_norm_w sink cache_lens block_table k_pages v_pages "
+                 "k_scale v_scale out lse workspace",
+                 (q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_pages, v_pages,
+                  k_scale, v_scale, out, lse, workspace))
 
     def call(st):
-        o = torch.empty((B, H, D), dtype=odt, device=dev) if out is None else out
-        ls = torch.empty((B, H), dtype=torch.float32, device=dev) if lse is None else lse
-        ws = alloc_decode_paged_workspace(B, H, Hk, dev) if workspace is None else workspace
-        _check(lib.flint_attn_decode_paged(
-            ctypes.byref(p), _addr(q), _addr(k), _addr(v), _addr(q_norm_w), _addr(k_norm_w),
-            _addr(sink), _addr(cache_lens), _addr(block_table), _addr(k_pages), _addr(v_pages),
-            _addr(k_scale), _addr(v_scale), _addr(o), _addr(ls), _addr(ws), ws.numel(), st),
-            "flint_attn_decode_paged")
+        o = q.new_empty((B, H, D), dtype=odt) if out is None else out
+        ls = sink.new_empty((B, H)) if lse is None else lse
+        ws = alloc_decode_paged_workspace(B, H, Hk) if workspace is None else workspace
+        code = lib.flint_attn_decode_paged(
+            p, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
+            sink.data_ptr(), cache_lens.data_ptr(), block_table.data_ptr(), k_pages.data_ptr(),
+            v_pages.data_ptr(), _addr(k_scale), _addr(v_scale), o.data_ptr(), ls.data_ptr(),
+            ws.data_ptr(), ws.numel(), st)
+        if code:
+            raise FlintError(code, "flint_attn_decode_paged")
         if check_status:
-            _check(lib.flint_attn_check_status(_addr(ws), st), "flint_attn_decode_paged (device)")
+            _check(lib.flint_attn_check_status(ws.data_ptr(), st),
+                   "flint_attn_decode_paged (device)")
         return o, ls
 
-    return _paged_call(dev, stream, call)
+    return _paged_call(index, stream, call)
 
 
 def exp2_poly(x: torch.Tensor) -> torch.Tensor:
