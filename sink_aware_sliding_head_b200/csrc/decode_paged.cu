@@ -35,8 +35,10 @@
 //     one A operand, so q keeps 16 bits of mantissa (22 over e4m3, whose
 //     products run in fp16) and the LSE stays exact to ~1e-6. O^T += V^T P^T
 //     has the heads as the MMA's N, and the P fragment that a lane holds is
-//     already the B operand. P is rounded to 16 bits for that product only; the
-//     row sums add the unrounded values. Over e4m3 the bytes become fp16 in
+//     already the B operand. P enters that product as fp16 over e4m3 and as a hi
+//     and a lo bf16 part over bf16 (with one part, 2^-8 of each weight, the error
+//     of a bf16 output rose by 1.4; the second product costs nothing next to the
+//     loads); the row sums add the unrounded values. Over e4m3 the bytes become fp16 in
 //     registers (exact), and the scales multiply S and O in FP32.
 //   * The new token never goes through the cache: its score is formed from the
 //     rounded row and enters when the warps of its segment are joined. Its row
@@ -694,7 +696,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
               }
             }
         }
-        uint32_t pb[4];
+        uint32_t pb[4], pl[4];                                 // P, and over bf16 what it leaves
         {
           float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
           mx = fmaxf(mx, fmaxf(fmaxf(sc[2][0], sc[2][1]), fmaxf(sc[3][0], sc[3][1])));
@@ -722,7 +724,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           for (int nt = 0; nt < 4; ++nt) {
             const float p0 = ex2_approx(sc[nt][0] - mb), p1 = ex2_approx(sc[nt][1] - mb);
             sum[nt] = p0 + p1;
-            pb[nt] = kF8 ? pack_f16x2(p0, p1) : pack_bf16x2(p0, p1);
+            if constexpr (kF8) pb[nt] = pack_f16x2(p0, p1);
+            else split_pair<false>(p0, p1, pb[nt], pl[nt]);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
@@ -762,6 +765,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 av.z &= vm[2 * c + 1]; av.w &= vm[2 * c + 1];
               }
               mma16816<kF8>(o[i], av, pb[2 * c], pb[2 * c + 1]);
+              mma16816<kF8>(o[i], av, pl[2 * c], pl[2 * c + 1]);
             }
           }
         }

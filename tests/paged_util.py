@@ -136,12 +136,13 @@ class Paged:
     def check_decode(self, out, lse, window, rows=None, scale=D ** -0.5):
         """out and lse (device tensors) against the formulas, by the roundings on the way.
 
-        The probabilities enter the second product in bf16 (relative 2^-8 each; 2^-11 over
-        e4m3 caches, whose products run in fp16) and carry the score error dz twice (in the
-        weight and in the sum); a bf16 out adds 2^-8 of its value.
+        The probabilities enter the second product as two bf16 parts (2^-16 of each; fp16,
+        2^-11, over e4m3 caches) and carry the score error dz twice (in the weight and in the
+        sum); sums and 2^x in 32 bits stay below 2^-18 of the sum of magnitudes; a bf16 out
+        adds 2^-8 of its value.
         """
         o, s = to64(out.float()), to64(lse)
-        p_step = 2.0 ** -11 if self.e4m3 else 2.0 ** -8
+        p_step = (2.0 ** -11 if self.e4m3 else 2.0 ** -16) + 2.0 ** -18
         for b in (range(len(self.lens)) if rows is None else rows):
             ro, rl, mag, dz = self.decode64(b, window, scale)
             tol = (p_step + 2 * dz[:, None]) * mag + 1e-30
