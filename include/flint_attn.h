@@ -260,7 +260,8 @@ flint_status_t flint_attn_decode(const flint_decode_params_t* params,
  *
  * Cache types: bfloat16, or e4m3 (one byte, 4 exponent and 3 mantissa bits, no
  * infinities), which holds x / scale[g] rounded to nearest even and saturated to
- * +-448, with one float per KV head for K and one for V (null: 1).
+ * +-448, with one float per KV head for K and one for V (null: 1; positive and
+ * normal: x is multiplied by its reciprocal, within 2^-22 of the quotient).
  *
  * cache_lens[b] is the number of tokens that sequence b has cached. -1 marks a
  * row that is not in use (a batch padded to a fixed size): nothing of it is read
@@ -340,8 +341,8 @@ typedef struct {
  * (0 if the params are invalid); 256-byte aligned. It must be zero before its
  * first use and serve no other entry point; every completed call leaves it ready
  * for the next one, whatever that call's sizes, so it is cleared once and not
- * per call. Calls that may overlap on the GPU (unordered streams) need one
- * workspace each. */
+ * per call (zero it again after a call that FLINT_ERR_TIMEOUT ended). Calls that
+ * may overlap on the GPU (unordered streams) need one workspace each. */
 size_t flint_attn_decode_paged_workspace_bytes(const flint_decode_paged_params_t* params);
 
 /* flint_attn_decode over a paged cache. Sequence b has p = cache_lens[b] tokens

@@ -583,7 +583,7 @@ def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, 
 
 
 def alloc_decode_paged_workspace(batch, num_q_heads, num_kv_heads, device=None) -> torch.Tensor:
-    """A zeroed workspace for ``decode_paged`` calls of up to this many rows.
+    """A zeroed workspace for ``decode_paged`` calls of up to this many rows and KV heads.
 
     One workspace serves any number of calls one after the other; calls that may
     overlap on the GPU need one each.
@@ -615,7 +615,7 @@ def decode_paged(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_p
     desc = _paged_cache(k_pages, v_pages, block_table, B, k_scale, v_scale)
     Hk, D = desc.num_kv_heads, desc.head_dim
     H = sink.numel()
-    p = DecodePagedParams(desc, B, H, window, 1 if use_rope else 0, rope_theta, rms_eps,
+    p = DecodePagedParams(desc, B, H, min(window, 0x7fffffff), 1 if use_rope else 0, rope_theta, rms_eps,
                           softmax_scale, FLINT_BF16, 1 if fp32_out else 0, 0,
                           _rows(q, "q", B, H, D), _rows(k, "k", B, Hk, D), _rows(v, "v", B, Hk, D))
     _vector(q_norm_w, "q_norm_w", torch.bfloat16, (D,))

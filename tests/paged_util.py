@@ -114,9 +114,9 @@ class Paged:
                         self.rope, THETA, 1e-6)[0]
         lo = max(0, p - window + 1) if window > 0 else 0
         pg, sl = self.slots(b, lo, p)
-        kp, vp = to64(self.kp.float()), to64(self.vp.float())
-        K = np.concatenate([kp[pg, :, sl], self.stored(kn[:1], sk)]) * sk[:, None]
-        V = np.concatenate([vp[pg, :, sl], self.stored(vn[:1], sv)]) * sv[:, None]
+        at = torch.as_tensor(pg, dtype=torch.long), slice(None), torch.as_tensor(sl)
+        K = np.concatenate([to64(self.kp[at].float()), self.stored(kn[:1], sk)]) * sk[:, None]
+        V = np.concatenate([to64(self.vp[at].float()), self.stored(vn[:1], sv)]) * sv[:, None]
         G = self.H // self.Hk
         out, lse = np.zeros((self.H, D)), np.zeros(self.H)
         mag, dz = np.zeros((self.H, D)), np.zeros(self.H)

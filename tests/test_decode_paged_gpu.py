@@ -54,6 +54,48 @@ def test_decode_ragged_batch_bf16_out(cuda_lib, dtype):
     assert out.dtype == BF16
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+@pytest.mark.parametrize("B,top,W", [(700, 150, 0), (1500, 40, 33)])
+def test_more_rows_than_a_block_keeps_lengths_of(cuda_lib, B, top, W, dtype):
+    lens = np.random.RandomState(B).randint(-1, top, B).tolist()
+    w = Paged(lens, H=2, Hk=1, P=16, dtype=dtype, seed=40)
+    d = w.dev()
+    out, lse = decode(cuda_lib, w, d, W, fp32_out=True)
+    rows = [b for b, p in enumerate(lens) if p >= 0]
+    w.check_pool(d["kp"], d["vp"], rows)
+    w.check_decode(out, lse, W, rows[:5] + rows[B // 2:B // 2 + 40] + rows[-40:])
+
+
+def test_a_range_of_more_rows_than_kept_lengths(cuda_lib):
+    """90000 rows on one KV head: over 512 rows to an SM's range, their lengths read late."""
+    B = 90000
+    lens = np.random.RandomState(1).randint(0, 3, B).tolist()
+    w = Paged(lens, H=1, Hk=1, P=16, seed=41, extra_cols=0)
+    d = w.dev()
+    out, lse = decode(cuda_lib, w, d, 0, fp32_out=True)
+    w.check_decode(out, lse, 0, list(range(0, B, 997)) + [B - 1])
+    assert torch.all(torch.isfinite(out)) and torch.all(torch.isfinite(lse))
+
+
+@pytest.mark.parametrize("lens", [[70], [333, 64]])
+def test_more_kv_heads_than_sms(cuda_lib, lens):
+    w = Paged(lens, H=200, Hk=200, P=16, seed=42)
+    check(cuda_lib, w, 100, fp32_out=True)
+
+
+@pytest.mark.parametrize("P", [80, 112, 272, 512])
+def test_page_sizes_off_the_block(cuda_lib, P):
+    w = Paged([P - 1, P, P + 1, 3 * P + 5], H=8, Hk=2, P=P, seed=43)
+    check(cuda_lib, w, 0, fp32_out=True)
+
+
+@pytest.mark.parametrize("lens", [[1], [64], [255], [256], [257], [2048], [9473]])
+def test_one_row_over_its_ranges(cuda_lib, lens):
+    """One row alone: its blocks end anywhere in the last range."""
+    w = Paged(lens, H=24, Hk=3, P=16, seed=44)
+    check(cuda_lib, w, 0, fp32_out=True)
+
+
 def test_rows_not_in_use_stay_as_they_were(cuda_lib):
     w = Paged([-1, 37, -1, 0, -1], P=16, seed=13)
     d = w.dev()
@@ -219,6 +261,32 @@ def test_two_graphs_share_a_workspace(cuda_lib):
     torch.cuda.synchronize()
     for w, (out, lse) in zip(cases, outs):
         w.check_decode(out, lse, 0)
+
+
+def test_a_captured_call_follows_its_lengths(cuda_lib):
+    """One capture, replayed after the lengths, the table and the new rows changed."""
+    runs = [Paged(lens, P=16, seed=45 + i, extra_cols=100 - max(lens) // 16)
+            for i, lens in enumerate([[10, 700, -1], [1500, 0, 63], [-1, -1, 64]])]
+    cols = min(w.table.shape[1] for w in runs)
+    pages = max(w.kp.shape[0] for w in runs)
+    d = runs[0].dev()
+    d["table"] = torch.zeros(3, cols, dtype=torch.int32, device="cuda")
+    d["kp"], d["vp"] = (torch.zeros(pages, 4, 16, 128, dtype=BF16, device="cuda") for _ in "kv")
+    ws = cuda_lib.alloc_decode_paged_workspace(3, 32, 4)
+    out, lse = torch.empty(3, 32, 128, device="cuda"), torch.empty(3, 32, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        decode(cuda_lib, runs[0], d, 0, check=False, fp32_out=True, out=out, lse=lse, workspace=ws)
+    for w in runs:
+        for name in ("q", "k", "v", "wq", "wk", "sink"):
+            d[name].copy_(getattr(w, name))
+        d["lens"].copy_(torch.tensor(w.lens, dtype=torch.int32))
+        d["table"].copy_(w.table[:, :cols])
+        d["kp"][:w.kp.shape[0]] = w.kp.cuda()
+        d["vp"][:w.vp.shape[0]] = w.vp.cuda()
+        graph.replay()
+        torch.cuda.synchronize()
+        w.check_decode(out, lse, 0, rows=[b for b, p in enumerate(w.lens) if p >= 0])
 
 
 @pytest.mark.parametrize("dtype", [BF16, E4M3])
