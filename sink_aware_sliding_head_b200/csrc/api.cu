@@ -193,15 +193,17 @@ bool encode_3d(CUtensorMap* m, const void* base, int T, int heads, int box_heads
 
 }  // namespace
 
-CUtensorMap paged_tensor_map(const PagedCache& c, const void* pool, int box, bool* ok) {
+CUtensorMap paged_tensor_map(const PagedCache& c, const void* pool, int box, long long apart,
+                             bool* ok) {
   CUtensorMap m{};
   EncodeTiledFn fn = encode_fn();
   if (!fn) { *ok = false; return m; }
   const cuuint64_t e = c.e4m3 ? 1 : 2;
-  const cuuint32_t halves = c.e4m3 ? 1 : 2;
+  const cuuint32_t halves = c.e4m3 && !apart ? 1 : 2;
   cuuint64_t dims[5] = {128 / e, (cuuint64_t)c.P, halves, (cuuint64_t)c.Hk,
                         (cuuint64_t)c.num_pages};
-  cuuint64_t strides[4] = {c.token_stride * e, 128, c.head_stride * e, c.page_stride * e};
+  cuuint64_t strides[4] = {c.token_stride * e, apart ? (cuuint64_t)apart : 128,
+                           c.head_stride * e, c.page_stride * e};
   cuuint32_t boxd[5] = {(cuuint32_t)(128 / e), (cuuint32_t)box, halves, 1, 1};
   cuuint32_t estr[5] = {1, 1, 1, 1, 1};
   const CUresult r = fn(&m, c.e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8

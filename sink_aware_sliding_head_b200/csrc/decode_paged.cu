@@ -19,12 +19,13 @@
 //     call follows its lengths and nothing but lens decides who sums what.
 //   * Loads. Two warps stream K and V of the range, a block each in turn, through
 //     a ring of shared memory with TMA, across segment borders, so that the ring
-//     fills while the math warps finish one segment and start the next. (Issuing a
-//     copy costs a warp 130 cycles or more: over 16-slot pages of e4m3 one warp
-//     alone took as long as its blocks' share of the HBM bandwidth twice over.)
-//     A tensor map in five dimensions (64 channels, slot, channel half, head,
-//     page) takes any page, head and token strides; a box is the largest power of
-//     two of slots that divides the page, at most 64, so no box crosses a page.
+//     fills while the math warps finish one segment and start the next. A tensor
+//     map in five dimensions (64 channels, slot, channel half, head, page) takes
+//     any page, head and token strides; a box is the largest power of two of slots
+//     that divides the page, at most 64, so no box crosses a page. Issuing a copy
+//     costs a warp 130 cycles or more, so e4m3, whose rows need no halves, takes
+//     that dimension for K and V and copies both at once (64 sequences, window
+//     4096, 16-slot pages: 58.2 us with a copy each, 54.0 with one for both).
 //   * Rows. With the rings of 148 SMs full, 19 MB are in flight and any load
 //     waits ~3 us behind them. Two more warps therefore fetch, normalise and
 //     rotate the q rows and the new row of the coming segments, up to four ahead,
@@ -94,7 +95,7 @@ struct Small {
 template <int NG, bool kF8>
 struct Cfg {
   static constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
-  static constexpr int kStageBytes = 2 * kBlk * kRowBytes;          // K, then V
+  static constexpr int kStageBytes = 2 * kBlk * kRowBytes;          // boxes of K and V rows
   // A pair's fixed cost in units. 201 rows of up to 2513 keys, nine heads to a KV
   // head, cost 0, 4, 8, 12: 54.1, 43.8, 44.8, - us in bf16, 58.4, 45.8, 44.9, 46.3
   // in e4m3; 250 rows of up to 900: 71.8, 53.2, 54.2, - and 76.0, 53.1, 47.5, 47.3.
@@ -121,6 +122,7 @@ struct Cfg {
 struct Args {
   PagedDecodeLaunch a;
   int box;                                   // slots per TMA box: 16, 32 or 64
+  int joint, v_first;                        // one copy for K and V; V's rows lie before K's
   uint32_t page_mul, page_shift;             // pos / P = umulhi(pos, page_mul) >> page_shift
   float scale_log2;
   int* counters;                             // [B * Hk], zero between calls
@@ -386,7 +388,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   if (warp >= kMathWarps + kRowWarps) {
     // ---------------------------------------------------------------- loads
     const int nbox = kBlk / A.box;                             // 1, 2 or 4 boxes a block
-    const uint32_t box_bytes = (uint32_t)A.box * C::kRowBytes;
+    const uint32_t box_bytes = (uint32_t)A.box * C::kRowBytes;  // of K; a box has K's and V's rows
     const uint32_t lw = warp - kMathWarps - kRowWarps;         // takes blocks n % kLoadWarps == lw
     uint32_t n = 0, issued = 0;                                // issued: its last block + 1
     bool ok = true;
@@ -440,9 +442,9 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         }
         __syncwarp();
         if (good) {
-          const uint32_t dst = smem_u32(smem + s * C::kStageBytes) + lane * box_bytes;
-          tma_load_5d(dst, &tm_k, full, slot, w.g, page);
-          tma_load_5d(dst + kBlk * C::kRowBytes, &tm_v, full, slot, w.g, page);
+          const uint32_t dst = smem_u32(smem + s * C::kStageBytes) + 2 * lane * box_bytes;
+          tma_load_5d(dst, &tm_k, full, slot, w.g, page);      // joint: V's rows with it
+          if (!A.joint) tma_load_5d(dst + box_bytes, &tm_v, full, slot, w.g, page);
         }
         __syncwarp();
         if (!looked) look_ahead();
@@ -609,10 +611,12 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int t8 = NG == 1 ? 0 : 8 * ((warp >> 1) & 1);          // the warp's first query head
   const uint32_t ring = smem_u32(smem);
   // 16 of the warp's keys lie in one box (boxes have 16, 32 or 64 slots)
+  const uint32_t box_bytes = (uint32_t)A.box * C::kRowBytes;
+  const uint32_t k_at = A.v_first ? box_bytes : 0, v_at = box_bytes - k_at;
   uint32_t chunk_at[2];
 #pragma unroll
   for (int c = 0; c < 2; ++c)
-    chunk_at[c] = (uint32_t)((key0 + 16 * c) / A.box) * A.box * C::kRowBytes +
+    chunk_at[c] = (uint32_t)((key0 + 16 * c) / A.box) * 2 * box_bytes +
                   (uint32_t)((key0 + 16 * c) % A.box) * 128;
   const uint32_t half_bytes = (uint32_t)A.box * 128;           // bf16: channels 64..127
   uint32_t n = 0;
@@ -647,7 +651,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       if (sm.bad[bar]) l = NAN;
       if (pos0 < p && pos0 + kKeys > lo) {
         const bool edge = pos0 < lo || pos0 + kKeys > p;
-        const uint32_t st = ring + s * C::kStageBytes;
+        const uint32_t st = ring + s * C::kStageBytes + k_at;
         // S of keys pos0 + 8 nt + 2 tig, + 1 for head gid: hi + lo parts
         float sc[4][2];
 #pragma unroll
@@ -729,7 +733,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
-        const uint32_t vst = st + kBlk * C::kRowBytes;
+        const uint32_t vst = ring + s * C::kStageBytes + v_at;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {                          // 16 keys
           if constexpr (kF8) {
@@ -970,9 +974,14 @@ cudaError_t launch_decode_paged(const PagedDecodeLaunch& a, int num_sms, cudaStr
   A.part_ml = reinterpret_cast<float*>(ws + 256);
   A.part_o = A.part_ml + rows * 2;
   A.counters = reinterpret_cast<int*>(ws + 256 + round256(rows * (2 + kHeadDim) * 4));
+  // The distance of the pools is a stride of the joint map (40 bits, not 0).
+  const long long apart = static_cast<char*>(a.c.v) - static_cast<char*>(a.c.k);
+  A.joint = a.c.e4m3 && apart != 0 && std::llabs(apart) < (1LL << 40);
+  A.v_first = A.joint && apart < 0;
   bool ok = true;
-  const CUtensorMap tk = paged_tensor_map(a.c, a.c.k, A.box, &ok);
-  const CUtensorMap tv = paged_tensor_map(a.c, a.c.v, A.box, &ok);
+  const CUtensorMap tk = paged_tensor_map(a.c, A.v_first ? a.c.v : a.c.k, A.box,
+                                          A.joint ? std::llabs(apart) : 0, &ok);
+  const CUtensorMap tv = A.joint ? tk : paged_tensor_map(a.c, a.c.v, A.box, 0, &ok);
   if (!ok) return cudaErrorInvalidValue;
   if (a.c.e4m3)
     return a.G <= 8 ? launch<1, true>(tk, tv, A, num_sms, st)

@@ -9,6 +9,7 @@
 // [pages, P, Hk, D] pools, or K and V interleaved in one tensor, are one case.
 #pragma once
 #include <cmath>
+#include <cstdlib>
 #include <cuda.h>
 #include <cuda_fp8.h>
 
@@ -224,7 +225,9 @@ size_t decode_paged_bytes(int B, int Hk, int num_sms);
 cudaError_t launch_decode_paged(const PagedDecodeLaunch& a, int num_sms, cudaStream_t st);
 // A pool as [page][head][half][slot][channels] with 128-byte rows (bf16: two
 // halves of 64 channels, e4m3: one of 128) and 128-byte swizzle; a box is `box`
-// slots of one head of one page, both halves. ok is cleared on failure.
-CUtensorMap paged_tensor_map(const PagedCache& c, const void* pool, int box, bool* ok);
+// slots of one head of one page, both halves. apart != 0 (e4m3): in place of the
+// halves, this pool and the one `apart` bytes behind it. ok is cleared on failure.
+CUtensorMap paged_tensor_map(const PagedCache& c, const void* pool, int box, long long apart,
+                             bool* ok);
 
 }  // namespace flint

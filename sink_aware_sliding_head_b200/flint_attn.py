@@ -519,6 +519,10 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+# the handle of a device's current stream, without a Stream object around it
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
 def _paged_call(index, stream, fn):
     """Runs ``fn(stream handle)`` with the tensors' device current and, for a given
     stream, that stream current too, so that what fn allocates belongs to it."""
@@ -531,8 +535,8 @@ def _paged_call(index, stream, fn):
             return fn(stream.cuda_stream)
     if index != torch.cuda.current_device():
         with torch.cuda.device(index):
-            return fn(torch.cuda.current_stream().cuda_stream)
-    return fn(torch.cuda.current_stream(index).cuda_stream)
+            return fn(_raw_stream(index))
+    return fn(_raw_stream(index))
 
 
 def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, v_pages, use_rope,
@@ -636,8 +640,8 @@ def decode_paged(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_p
                   k_scale, v_scale, out, lse, workspace))
 
     def call(st):
-        o = q.new_empty((B, H, D), dtype=odt) if out is None else out
-        ls = sink.new_empty((B, H)) if lse is None else lse
+        o = q.new_empty(B, H, D, dtype=odt) if out is None else out
+        ls = sink.new_empty(B, H) if lse is None else lse
         ws = alloc_decode_paged_workspace(B, H, Hk) if workspace is None else workspace
         code = lib.flint_attn_decode_paged(
             p, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),

@@ -38,6 +38,7 @@ def check(fa, w, window, **kw):
     ([1099, 513, 1024], 32, 4, 64, 1000, "token", False),
     ([4000], 16, 1, 16, 0, "head", True),                     # one pair over many splits
     ([70000], 2, 1, 128, 0, "head", True),                    # a far position
+    ([9000], 16, 1, 64, 0, "head", True),                     # 36 and more partials, G = 16
 ])
 def test_decode_matches_the_formulas(cuda_lib, lens, H, Hk, P, W, layout, rope, dtype):
     w = Paged(lens, H=H, Hk=Hk, P=P, dtype=dtype, layout=layout, rope=rope, seed=11)
@@ -94,6 +95,21 @@ def test_one_row_over_its_ranges(cuda_lib, lens):
     """One row alone: its blocks end anywhere in the last range."""
     w = Paged(lens, H=24, Hk=3, P=16, seed=44)
     check(cuda_lib, w, 0, fp32_out=True)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_pools_in_either_order(cuda_lib, dtype):
+    """V's pool before K's in memory, as well as behind it."""
+    for flip in (False, True):
+        w = Paged([200, 31], H=8, Hk=2, P=16, dtype=dtype, seed=48)
+        d = w.dev()
+        one = torch.empty(2, *w.kp.shape, dtype=dtype, device="cuda")
+        one[int(flip)].copy_(d["kp"])
+        one[1 - int(flip)].copy_(d["vp"])
+        d["kp"], d["vp"] = one[int(flip)], one[1 - int(flip)]
+        out, lse = decode(cuda_lib, w, d, 0, fp32_out=True)
+        w.check_decode(out, lse, 0)
+        w.check_pool(d["kp"], d["vp"])
 
 
 def test_rows_not_in_use_stay_as_they_were(cuda_lib):
