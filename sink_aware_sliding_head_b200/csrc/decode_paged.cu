@@ -873,10 +873,11 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const Part q = i ? last_part : first_part;
     int last = 0;
     if (q.b >= 0) {
-      __threadfence();
       int* counter = A.counters + (long long)q.b * a.c.Hk + q.g;
-      if (atomicAdd(counter, 1) == q.c1 - q.c0) {
-        __threadfence();
+      int arrived;                                             // releases this block's partial,
+      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;"   // acquires the others'
+                   : "=r"(arrived) : "l"(counter) : "memory");
+      if (arrived == q.c1 - q.c0) {
         *counter = 0;                                          // ready for the next call
         last = 1;
       }
