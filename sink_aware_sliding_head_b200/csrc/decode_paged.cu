@@ -48,8 +48,8 @@
 //     is stored after the segment's last load has landed.
 //
 // Measured (B200, 6.56 TB/s copy): 64 sequences of 4096 visible keys, 32 query and
-// 4 KV heads, 90 us in bf16 (6.0 TB/s), 54 us in e4m3 (5.0 TB/s); four sequences
-// near 131072 keys 142 us (6.6 TB/s); one row of 230 keys 6.7 us. The fixed part is
+// 4 KV heads, 89 us in bf16 (6.0 TB/s), 53 us in e4m3 (5.1 TB/s); four sequences
+// near 131072 keys 141 us (6.7 TB/s); one row of 230 keys 6.1 us. The fixed part is
 // ~5 us: the plan, the first rows and pages (each a trip to HBM), and the join.
 #include "paged.cuh"
 #include "sm100_primitives.cuh"
@@ -303,6 +303,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+
+  previous_done();
 
   // ---- the plan: all units, and where this block's range begins
   Walk w;
@@ -954,8 +956,7 @@ cudaError_t launch(const CUtensorMap& tk, const CUtensorMap& tv, const Args& A, 
   cudaError_t e = smem_limit_once(once, decode_paged_kernel<NG, kF8>, bytes);
   if (e != cudaSuccess) return e;
   ProfScope prof(kKDecodePaged, st);
-  decode_paged_kernel<NG, kF8><<<grid, kThreads, bytes, st>>>(tk, tv, A);
-  return cudaGetLastError();
+  return launch_overlapped(decode_paged_kernel<NG, kF8>, grid, kThreads, bytes, st, tk, tv, A);
 }
 
 }  // namespace

@@ -12,6 +12,12 @@
 // angles (four a lane, shared by all heads) while they come, and needs neither
 // shared memory nor a barrier. Blocks are persistent, so a lane forms its four
 // frequencies once.
+//
+// Measured (B200, 6.56 TB/s copy): 65536 prompt tokens of 4 KV heads 46 us (5.8
+// TB/s), 131072 without RoPE 88 us (6.1 TB/s); 22539 tokens of 8 heads to e4m3 37 us
+// (3.8 TB/s: the instructions of the conversions and waits for loads bound it).
+// Requesting the next token's rows before the current one's are done was slower
+// (65536 tokens: 55 us).
 #include "paged.cuh"
 
 namespace flint {
@@ -26,6 +32,7 @@ template <bool kE4m3>
 __global__ void __launch_bounds__(kThreads, kBlocks)
 paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
   const int l = threadIdx.x & 15;
+  previous_done();
   const RowPart w = unpack_row(load_row(a.wk));
   double f[4];
 #pragma unroll
@@ -99,9 +106,8 @@ cudaError_t launch_paged_append(const PagedAppendLaunch& a, int num_sms, cudaStr
   // its instructions: one (22539 tokens: 36.6 us, with four 39.3).
   const int most = kBlocks * num_sms * (a.c.e4m3 ? 1 : 4);
   const int grid = blocks < most ? blocks : most;
-  if (a.c.e4m3) paged_append_kernel<true><<<grid, kThreads, 0, st>>>(a);
-  else paged_append_kernel<false><<<grid, kThreads, 0, st>>>(a);
-  return cudaGetLastError();
+  return launch_overlapped(a.c.e4m3 ? paged_append_kernel<true> : paged_append_kernel<false>,
+                           grid, kThreads, 0, st, a);
 }
 
 }  // namespace flint
