@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import struct
 from typing import Optional
 
 import torch
@@ -125,6 +126,12 @@ class DecodePagedParams(ctypes.Structure):
     ]
 
 
+# The same two structures as packed by a call: a third of the time of building a
+# ctypes structure.
+_PACK_APPEND = struct.Struct("@6i4q3i2fi2q").pack
+_PACK_DECODE = struct.Struct("@6i4q4i3f3i3q").pack
+
+
 class FlintError(RuntimeError):
     def __init__(self, code: int, where: str):
         super().__init__(f"{where}: {STATUS.get(code, code)}")
@@ -182,12 +189,12 @@ def load_library(path: str = LIB_PATH):
     lib.flint_attn_decode_workspace_bytes.restype = sz
     lib.flint_attn_decode.argtypes = [DP] + [vp] * 11 + [vp, sz, vp]
     lib.flint_attn_decode.restype = ctypes.c_int
-    lib.flint_attn_paged_append.argtypes = [ctypes.POINTER(PagedAppendParams)] + [vp] * 12
+    # (the params of the paged calls: a structure by reference, or its bytes)
+    lib.flint_attn_paged_append.argtypes = [vp] * 13
     lib.flint_attn_paged_append.restype = ctypes.c_int
-    PP = ctypes.POINTER(DecodePagedParams)
-    lib.flint_attn_decode_paged_workspace_bytes.argtypes = [PP]
+    lib.flint_attn_decode_paged_workspace_bytes.argtypes = [vp]
     lib.flint_attn_decode_paged_workspace_bytes.restype = sz
-    lib.flint_attn_decode_paged.argtypes = [PP] + [vp] * 15 + [sz, vp]
+    lib.flint_attn_decode_paged.argtypes = [vp] * 16 + [sz, vp]
     lib.flint_attn_decode_paged.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -475,7 +482,8 @@ def _pool_strides(t):
     return tuple(D if n == 1 else st for n, st in zip(t.shape[:3], t.stride())) + t.stride()[3:]
 
 
-def _paged_cache(k_pages, v_pages, block_table, rows, k_scale, v_scale) -> PagedCacheDesc:
+def _paged_cache(k_pages, v_pages, block_table, rows, k_scale, v_scale):
+    """The fields of ``flint_paged_cache_t``, in order."""
     shape, dtype = k_pages.shape, k_pages.dtype
     if len(shape) != 4 or v_pages.shape != shape or v_pages.dtype is not dtype:
         raise ValueError("k_pages and v_pages must be [pages, Hk, page_size, D] of one type, got "
@@ -512,7 +520,7 @@ def _paged_cache(k_pages, v_pages, block_table, rows, k_scale, v_scale) -> Paged
     if (col != 1 and cols > 1) or (row < cols and rows > 1):
         raise ValueError("block_table: the entries of a row must be contiguous and rows not "
                          f"overlap, got strides {block_table.stride()}")
-    return PagedCacheDesc(n, P, cols, Hk, D, code, page, head, slot, row if rows > 1 else 0)
+    return n, P, cols, Hk, D, code, page, head, slot, row if rows > 1 else 0
 
 
 def _addr(t):
@@ -523,20 +531,19 @@ def _addr(t):
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _paged_call(index, stream, fn):
-    """Runs ``fn(stream handle)`` with the tensors' device current and, for a given
-    stream, that stream current too, so that what fn allocates belongs to it."""
+def _elsewhere(index, stream):
+    """The context in which a call's allocations belong to its stream (or None where they
+    do already), and the stream's handle."""
     if index < 0:
         raise ValueError("CUDA tensors expected")
     if stream is not None:
         if stream.device_index != index:
-            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on cuda:{index}")
-        with torch.cuda.stream(stream):
-            return fn(stream.cuda_stream)
+            raise ValueError(f"stream is on cuda:{stream.device_index}, the tensors on "
+                             f"cuda:{index}")
+        return torch.cuda.stream(stream), stream.cuda_stream
     if index != torch.cuda.current_device():
-        with torch.cuda.device(index):
-            return fn(_raw_stream(index))
-    return fn(_raw_stream(index))
+        return torch.cuda.device(index), _raw_stream(index)
+    return None, _raw_stream(index)
 
 
 def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, v_pages, use_rope,
@@ -554,11 +561,11 @@ def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, 
     [64] zeroed once by the caller, where device-side errors collect (a fresh one if
     omitted); ``check_status`` synchronises and raises ``FlintError`` for them.
     """
-    lib = load_library()
     N, T = cache_lens.numel(), k.shape[0]
     desc = _paged_cache(k_pages, v_pages, block_table, N, k_scale, v_scale)
-    Hk, D = desc.num_kv_heads, desc.head_dim
-    k_stride, v_stride = _rows(k, "k", T, Hk, D), _rows(v, "v", T, Hk, D)
+    Hk, D = desc[3], desc[4]
+    params = _PACK_APPEND(*desc, N, T, 1 if use_rope else 0, rope_theta, rms_eps, FLINT_BF16,
+                          _rows(k, "k", T, Hk, D), _rows(v, "v", T, Hk, D))
     _vector(k_norm_w, "k_norm_w", torch.bfloat16, (D,))
     _vector(cache_lens, "cache_lens", torch.int32, (N,))
     _vector(cu_new_lens, "cu_new_lens", torch.int32, (N + 1,))
@@ -568,22 +575,29 @@ def paged_append(k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, 
     _same_device(index, "k v k_norm_w cu_new_lens cache_lens block_table k_pages v_pages k_scale "
                  "v_scale status", (k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages,
                                     v_pages, k_scale, v_scale, status))
-    p = PagedAppendParams(desc, N, T, 1 if use_rope else 0, rope_theta, rms_eps, FLINT_BF16,
-                          k_stride, v_stride)
+    where, handle = _elsewhere(index, stream)
+    if where is not None:
+        with where:
+            return _launch_append(params, k, v, k_norm_w, cu_new_lens, cache_lens, block_table,
+                                  k_pages, v_pages, k_scale, v_scale, status, handle, check_status)
+    return _launch_append(params, k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages,
+                          v_pages, k_scale, v_scale, status, handle, check_status)
 
-    def call(st):
-        word = torch.zeros(64, dtype=torch.int32, device=k_pages.device) if status is None else status
-        code = lib.flint_attn_paged_append(
-            p, k.data_ptr(), v.data_ptr(), k_norm_w.data_ptr(), cu_new_lens.data_ptr(),
-            cache_lens.data_ptr(), block_table.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-            _addr(k_scale), _addr(v_scale), word.data_ptr(), st)
-        if code:
-            raise FlintError(code, "flint_attn_paged_append")
-        if check_status:
-            _check(lib.flint_attn_check_status(word.data_ptr(), st),
-                   "flint_attn_paged_append (device)")
 
-    _paged_call(index, stream, call)
+def _launch_append(params, k, v, k_norm_w, cu_new_lens, cache_lens, block_table, k_pages, v_pages,
+                   k_scale, v_scale, status, handle, check_status):
+    lib = load_library()
+    if status is None:
+        status = torch.zeros(64, dtype=torch.int32, device=k_pages.device)
+    code = lib.flint_attn_paged_append(
+        params, k.data_ptr(), v.data_ptr(), k_norm_w.data_ptr(), cu_new_lens.data_ptr(),
+        cache_lens.data_ptr(), block_table.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        _addr(k_scale), _addr(v_scale), status.data_ptr(), handle)
+    if code:
+        raise FlintError(code, "flint_attn_paged_append")
+    if check_status:
+        _check(lib.flint_attn_check_status(status.data_ptr(), handle),
+               "flint_attn_paged_append (device)")
 
 
 def alloc_decode_paged_workspace(batch, num_q_heads, num_kv_heads, device=None) -> torch.Tensor:
@@ -614,21 +628,18 @@ def decode_paged(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_p
     (out [B,H,D], lse [B,H] fp32). ``workspace``: from
     ``alloc_decode_paged_workspace``, kept between calls (a fresh one if omitted).
     """
-    lib = load_library()
-    B = cache_lens.numel()
+    B, H = cache_lens.numel(), sink.numel()
     desc = _paged_cache(k_pages, v_pages, block_table, B, k_scale, v_scale)
-    Hk, D = desc.num_kv_heads, desc.head_dim
-    H = sink.numel()
-    p = DecodePagedParams(desc, B, H, min(window, 0x7fffffff), 1 if use_rope else 0, rope_theta, rms_eps,
-                          softmax_scale, FLINT_BF16, 1 if fp32_out else 0, 0,
+    Hk, D = desc[3], desc[4]
+    params = _PACK_DECODE(*desc, B, H, max(-1, min(window, 0x7fffffff)), 1 if use_rope else 0,
+                          rope_theta, rms_eps, softmax_scale, FLINT_BF16, 1 if fp32_out else 0, 0,
                           _rows(q, "q", B, H, D), _rows(k, "k", B, Hk, D), _rows(v, "v", B, Hk, D))
     _vector(q_norm_w, "q_norm_w", torch.bfloat16, (D,))
     _vector(k_norm_w, "k_norm_w", torch.bfloat16, (D,))
     _vector(sink, "sink", torch.float32, (H,))
     _vector(cache_lens, "cache_lens", torch.int32, (B,))
-    odt = torch.float32 if fp32_out else torch.bfloat16
     if out is not None:
-        _vector(out, "out", odt, (B, H, D))
+        _vector(out, "out", torch.float32 if fp32_out else torch.bfloat16, (B, H, D))
     if lse is not None:
         _vector(lse, "lse", torch.float32, (B, H))
     if workspace is not None:
@@ -638,24 +649,37 @@ def decode_paged(q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_p
                  "k_scale v_scale out lse workspace",
                  (q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_pages, v_pages,
                   k_scale, v_scale, out, lse, workspace))
+    args = (params, q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_pages, v_pages,
+            k_scale, v_scale, out, lse, workspace)
+    where, handle = _elsewhere(index, stream)
+    if where is not None:
+        with where:
+            return _launch_decode(*args, handle, check_status, fp32_out, (B, H, Hk, D))
+    return _launch_decode(*args, handle, check_status, fp32_out, (B, H, Hk, D))
 
-    def call(st):
-        o = q.new_empty(B, H, D, dtype=odt) if out is None else out
-        ls = sink.new_empty(B, H) if lse is None else lse
-        ws = alloc_decode_paged_workspace(B, H, Hk) if workspace is None else workspace
-        code = lib.flint_attn_decode_paged(
-            p, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(), k_norm_w.data_ptr(),
-            sink.data_ptr(), cache_lens.data_ptr(), block_table.data_ptr(), k_pages.data_ptr(),
-            v_pages.data_ptr(), _addr(k_scale), _addr(v_scale), o.data_ptr(), ls.data_ptr(),
-            ws.data_ptr(), ws.numel(), st)
-        if code:
-            raise FlintError(code, "flint_attn_decode_paged")
-        if check_status:
-            _check(lib.flint_attn_check_status(ws.data_ptr(), st),
-                   "flint_attn_decode_paged (device)")
-        return o, ls
 
-    return _paged_call(index, stream, call)
+def _launch_decode(params, q, k, v, q_norm_w, k_norm_w, sink, cache_lens, block_table, k_pages,
+                   v_pages, k_scale, v_scale, out, lse, workspace, handle, check_status, fp32_out,
+                   sizes):
+    lib = load_library()
+    B, H, Hk, D = sizes
+    if out is None:
+        out = sink.new_empty(B, H, D) if fp32_out else q.new_empty(B, H, D)
+    if lse is None:
+        lse = sink.new_empty(B, H)
+    if workspace is None:
+        workspace = alloc_decode_paged_workspace(B, H, Hk)
+    code = lib.flint_attn_decode_paged(
+        params, q.data_ptr(), k.data_ptr(), v.data_ptr(), q_norm_w.data_ptr(),
+        k_norm_w.data_ptr(), sink.data_ptr(), cache_lens.data_ptr(), block_table.data_ptr(),
+        k_pages.data_ptr(), v_pages.data_ptr(), _addr(k_scale), _addr(v_scale), out.data_ptr(),
+        lse.data_ptr(), workspace.data_ptr(), workspace.numel(), handle)
+    if code:
+        raise FlintError(code, "flint_attn_decode_paged")
+    if check_status:
+        _check(lib.flint_attn_check_status(workspace.data_ptr(), handle),
+               "flint_attn_decode_paged (device)")
+    return out, lse
 
 
 def exp2_poly(x: torch.Tensor) -> torch.Tensor:

@@ -150,6 +150,41 @@ def test_bad_append_pointers(lib):
     assert call_append(lib, none, k=None, v=None, kp=None) == INVALID
 
 
+def test_packed_params_match_the_structures():
+    """The bytes that a call packs are the ctypes structures' (and so the header's)."""
+    desc = (8, 16, 4, 2, 128, 1, 8192, 4096, 256, 5)
+    assert fa._PACK_APPEND(*desc, 3, 7, 1, 1e6, 1e-6, 0, 512, 520) == \
+        bytes(fa.PagedAppendParams(fa.PagedCacheDesc(*desc), 3, 7, 1, 1e6, 1e-6, 0, 512, 520))
+    assert fa._PACK_DECODE(*desc, 3, 32, 9, 1, 1e6, 1e-6, 0.5, 0, 1, 0, 4096, 512, 520) == \
+        bytes(fa.DecodePagedParams(fa.PagedCacheDesc(*desc), 3, 32, 9, 1, 1e6, 1e-6, 0.5, 0, 1, 0,
+                                   4096, 512, 520))
+
+
+def test_structures_match_the_header(lib, tmp_path):
+    """Sizes and offsets of the paged structures as a C compiler sees them."""
+    import os
+    import shutil
+    import subprocess
+    gcc = shutil.which("gcc")
+    if gcc is None:
+        pytest.skip("no C compiler")
+    fields = [("flint_paged_cache_t", fa.PagedCacheDesc),
+              ("flint_paged_append_params_t", fa.PagedAppendParams),
+              ("flint_decode_paged_params_t", fa.DecodePagedParams)]
+    body = "".join(f'printf("%zu ", offsetof({c}, {n}));' for c, s in fields for n, _ in s._fields_)
+    body += "".join(f'printf("%zu ", sizeof({c}));' for c, _ in fields)
+    src = tmp_path / "layout.c"
+    src.write_text("#include <stddef.h>\n#include <stdio.h>\n#include \"flint_attn.h\"\n"
+                   "int main(void) {" + body + "return 0; }\n")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    subprocess.run([gcc, "-std=c99", "-Wall", "-Werror", "-I", os.path.join(root, "include"),
+                    str(src), "-o", str(tmp_path / "layout")], check=True)
+    got = subprocess.run([str(tmp_path / "layout")], capture_output=True, text=True).stdout
+    want = [getattr(s, n).offset for _, s in fields for n, _ in s._fields_]
+    want += [ctypes.sizeof(s) for _, s in fields]
+    assert list(map(int, got.split())) == want
+
+
 def tensors(**kw):
     bf = torch.bfloat16
     t = dict(q=torch.zeros(2, 32, 128, dtype=bf), k=torch.zeros(2, 4, 128, dtype=bf),
