@@ -8,14 +8,14 @@
 //
 // Bound by HBM: 512 bytes of K and V read per (token, KV head) and 512 (bf16)
 // or 256 (e4m3) written, against ~100 operations. A half-warp takes a token: it
-// requests the rows of up to kHeads heads, then finds the token's slot and its 64
+// requests the rows of 4 or 8 heads, then finds the token's slot and its 64
 // angles (four a lane, shared by all heads) while they come, and needs neither
 // shared memory nor a barrier. Blocks are persistent, so a lane forms its four
 // frequencies once.
 //
 // Measured (B200, 6.56 TB/s copy): 65536 prompt tokens of 4 KV heads 46 us (5.8
-// TB/s), 131072 without RoPE 88 us (6.1 TB/s); 22539 tokens of 8 heads to e4m3 37 us
-// (3.8 TB/s: the instructions of the conversions and waits for loads bound it).
+// TB/s), 131072 without RoPE 88 us (6.1 TB/s); 22539 tokens of 8 heads to e4m3 32 us
+// (4.4 TB/s: the instructions of the conversions and waits for loads bound it).
 // Requesting the next token's rows before the current one's are done was slower
 // (65536 tokens: 55 us).
 #include "paged.cuh"
@@ -25,11 +25,16 @@ namespace flint {
 namespace {
 
 constexpr int kThreads = 128;                // 8 tokens at a time
-constexpr int kHeads = 4;                    // heads in flight: 16 loads of 8 bytes a lane
-constexpr int kBlocks = 5;                   // per SM
 
-template <bool kE4m3>
-__global__ void __launch_bounds__(kThreads, kBlocks)
+// Heads whose rows are in flight together (four loads of 8 bytes a lane each) and
+// blocks per SM. Up to 4 KV heads 4, with more of them 8: eight heads in two turns
+// of 4 against one of 8 took 53.4 and 46.4 us (32000 tokens, bf16), 37.1 and 31.7
+// (22539 to e4m3); four heads 46.2 and 47.9 us (65536 tokens, bf16).
+constexpr int heads_at_once(int Hk) { return Hk <= 4 ? 4 : 8; }
+constexpr int blocks_per_sm(int heads) { return heads == 4 ? 5 : 4; }
+
+template <bool kE4m3, int kHeads>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(kHeads))
 paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
   const int l = threadIdx.x & 15;
   previous_done();
@@ -104,10 +109,12 @@ cudaError_t launch_paged_append(const PagedAppendLaunch& a, int num_sms, cudaStr
   // (131072 tokens: 96.7 us with one, 88.2 with four, 83.4 with all; 65536 of one
   // KV head 24.2, 25.4, 28.3: every block forms its frequencies). e4m3 is bound by
   // its instructions: one (22539 tokens: 36.6 us, with four 39.3).
-  const int most = kBlocks * num_sms * (a.c.e4m3 ? 1 : 4);
+  const int heads = heads_at_once(a.c.Hk);
+  const int most = blocks_per_sm(heads) * num_sms * (a.c.e4m3 ? 1 : 4);
   const int grid = blocks < most ? blocks : most;
-  return launch_overlapped(a.c.e4m3 ? paged_append_kernel<true> : paged_append_kernel<false>,
-                           grid, kThreads, 0, st, a);
+  auto kernel = heads == 4 ? (a.c.e4m3 ? paged_append_kernel<true, 4> : paged_append_kernel<false, 4>)
+                           : (a.c.e4m3 ? paged_append_kernel<true, 8> : paged_append_kernel<false, 8>);
+  return launch_overlapped(kernel, grid, kThreads, 0, st, a);
 }
 
 }  // namespace flint
