@@ -8,7 +8,7 @@
 //
 // Bound by HBM: 512 bytes of K and V read per (token, KV head) and 512 (bf16)
 // or 256 (e4m3) written, against ~100 operations. A half-warp takes a token: it
-// requests the rows of 4 or 8 heads, then finds the token's slot and its 64
+// requests the rows of up to 8 heads, then finds the token's slot and its 64
 // angles (four a lane, shared by all heads) while they come, and needs neither
 // shared memory nor a barrier. Blocks are persistent, so a lane forms its four
 // frequencies once.
@@ -17,7 +17,8 @@
 // TB/s), 131072 without RoPE 88 us (6.1 TB/s); 22539 tokens of 8 heads to e4m3 32 us
 // (4.4 TB/s: the instructions of the conversions and waits for loads bound it).
 // Requesting the next token's rows before the current one's are done was slower
-// (65536 tokens: 55 us).
+// (65536 tokens: 55 us), and so were four tokens a half-warp at a time where there
+// is one KV head (65536 tokens: 25.3 us with one, 26.1 with four).
 #include "paged.cuh"
 
 namespace flint {
@@ -26,12 +27,14 @@ namespace {
 
 constexpr int kThreads = 128;                // 8 tokens at a time
 
-// Heads whose rows are in flight together (four loads of 8 bytes a lane each) and
-// blocks per SM. Up to 4 KV heads 4, with more of them 8: eight heads in two turns
-// of 4 against one of 8 took 53.4 and 46.4 us (32000 tokens, bf16), 37.1 and 31.7
-// (22539 to e4m3); four heads 46.2 and 47.9 us (65536 tokens, bf16).
-constexpr int heads_at_once(int Hk) { return Hk <= 4 ? 4 : 8; }
-constexpr int blocks_per_sm(int heads) { return heads == 4 ? 5 : 4; }
+// Heads whose rows are in flight together (four loads of 8 bytes a lane each), and
+// blocks per SM by the registers that takes. Eight heads in two turns of 4 against
+// one of 8 took 53.4 and 46.4 us (32000 tokens, bf16), 37.1 and 31.7 (22539 to
+// e4m3); four heads in a turn of 4 or half a turn of 8 46.2 and 47.9 us (65536 tokens,
+// bf16); one head in a quarter of a turn of 4 or a turn of its own 25.2 and 21.3, two 31.2 and 27.0.
+constexpr int blocks_per_sm(int heads) {
+  return heads <= 2 ? 8 : heads == 4 ? 5 : 4;
+}
 
 template <bool kE4m3, int kHeads>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(kHeads))
@@ -109,12 +112,16 @@ cudaError_t launch_paged_append(const PagedAppendLaunch& a, int num_sms, cudaStr
   // (131072 tokens: 96.7 us with one, 88.2 with four, 83.4 with all; 65536 of one
   // KV head 24.2, 25.4, 28.3: every block forms its frequencies). e4m3 is bound by
   // its instructions: one (22539 tokens: 36.6 us, with four 39.3).
-  const int heads = heads_at_once(a.c.Hk);
-  const int most = blocks_per_sm(heads) * num_sms * (a.c.e4m3 ? 1 : 4);
+  typedef void (*Kernel)(PagedAppendLaunch);
+  static const Kernel kernels[2][4] = {
+      {paged_append_kernel<false, 1>, paged_append_kernel<false, 2>,
+       paged_append_kernel<false, 4>, paged_append_kernel<false, 8>},
+      {paged_append_kernel<true, 1>, paged_append_kernel<true, 2>,
+       paged_append_kernel<true, 4>, paged_append_kernel<true, 8>}};
+  const int v = a.c.Hk == 1 ? 0 : a.c.Hk == 2 ? 1 : a.c.Hk <= 4 ? 2 : 3;
+  const int most = blocks_per_sm(1 << v) * num_sms * (a.c.e4m3 ? 1 : 4);
   const int grid = blocks < most ? blocks : most;
-  auto kernel = heads == 4 ? (a.c.e4m3 ? paged_append_kernel<true, 4> : paged_append_kernel<false, 4>)
-                           : (a.c.e4m3 ? paged_append_kernel<true, 8> : paged_append_kernel<false, 8>);
-  return launch_overlapped(kernel, grid, kThreads, 0, st, a);
+  return launch_overlapped(kernels[a.c.e4m3][v], grid, kThreads, 0, st, a);
 }
 
 }  // namespace flint
