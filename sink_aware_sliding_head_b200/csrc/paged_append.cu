@@ -30,8 +30,9 @@ constexpr int kThreads = 128;                // 8 tokens at a time
 // Heads whose rows are in flight together (four loads of 8 bytes a lane each), and
 // blocks per SM by the registers that takes. Eight heads in two turns of 4 against
 // one of 8 took 53.4 and 46.4 us (32000 tokens, bf16), 37.1 and 31.7 (22539 to
-// e4m3); four heads in a turn of 4 or half a turn of 8 46.2 and 47.9 us (65536 tokens,
-// bf16); one head in a quarter of a turn of 4 or a turn of its own 25.2 and 21.3, two 31.2 and 27.0.
+// e4m3); four heads in a turn of 4 or half a turn of 8 46.2 and 47.9 us (65536
+// tokens, bf16); one head in a quarter of a turn of 4 or a turn of its own 25.2 and
+// 21.3, two 31.2 and 27.0.
 constexpr int blocks_per_sm(int heads) {
   return heads <= 2 ? 8 : heads == 4 ? 5 : 4;
 }
@@ -110,8 +111,9 @@ cudaError_t launch_paged_append(const PagedAppendLaunch& a, int num_sms, cudaStr
   const int blocks = (int)(((long long)a.T + per - 1) / per);
   // bf16, bound by HBM: four times the resident blocks, which even out the SMs
   // (131072 tokens: 96.7 us with one, 88.2 with four, 83.4 with all; 65536 of one
-  // KV head 24.2, 25.4, 28.3: every block forms its frequencies). e4m3 is bound by
-  // its instructions: one (22539 tokens: 36.6 us, with four 39.3).
+  // KV head, four in flight, 24.2, 25.4, 28.3: every block forms its frequencies).
+  // e4m3 is bound by its instructions: one (22539 tokens, four heads in flight,
+  // 36.6 us, with four 39.3).
   typedef void (*Kernel)(PagedAppendLaunch);
   static const Kernel kernels[2][4] = {
       {paged_append_kernel<false, 1>, paged_append_kernel<false, 2>,
