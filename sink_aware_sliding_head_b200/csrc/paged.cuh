@@ -197,8 +197,9 @@ __device__ __forceinline__ void store_row(void* pool, long long off, RowBits b) 
 // ------------------------------------------------------------------ launchers
 // Both kernels are launched so that their blocks may be set up while the kernel
 // before them on the stream drains; previous_done() waits for that kernel's end
-// (and its writes) and precedes every access to global memory. Back to back calls take 1 to 2 us less each
-// (64 sequences, window 4096: 92.0 -> 90.6 us; 201 ragged rows 43.0 -> 41.1).
+// (and its writes) and precedes every access to global memory. Back to back calls
+// take 1 to 2 us less each (64 sequences, window 4096: 92.0 -> 90.6 us; 201 ragged
+// rows 43.0 -> 41.1).
 __device__ __forceinline__ void previous_done() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
