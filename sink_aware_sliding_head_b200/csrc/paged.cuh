@@ -64,7 +64,13 @@ __device__ __forceinline__ double rope_turns(int j, const RopePowers& w) {
 __device__ __forceinline__ void rope_cos_sin(int pos, double f, float* c, float* s) {
   double turns = (double)pos * f;
   turns -= rint(turns);
-  sincospif(2.f * (float)turns, s, c);
+  const float t = (float)turns;
+  float s0, c0;
+  sincospif(2.f * t, &s0, &c0);
+  // what the float left out of the angle, to first order (up to 2^-25 of a turn)
+  const float d = 6.2831853f * (float)(turns - (double)t);
+  *s = fmaf(c0, d, s0);
+  *c = fmaf(-s0, d, c0);
 }
 
 // A row of 128 channels belongs to a half-warp: lane l has channels 4l .. 4l+3 (x[0])

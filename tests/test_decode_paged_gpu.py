@@ -112,6 +112,36 @@ def test_pools_in_either_order(cuda_lib, dtype):
         w.check_pool(d["kp"], d["vp"])
 
 
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_offsets_past_32_bits(cuda_lib, dtype):
+    """Pages that lie more than 2^32 bytes (and 2^31 elements) into their pool."""
+    w = Paged([200, 31, 77], new=[1, 1, 1], H=8, Hk=2, P=16, dtype=dtype, seed=49)
+    d = w.dev()
+    n = w.kp.shape[0]
+    pages = (1 << 32) // (2 * 16 * 128) + n + 1                # of 4096 elements
+    far = torch.arange(pages - n, pages, device="cuda")
+    pools = []
+    for x in (d["kp"], d["vp"]):
+        big = torch.empty(pages, 2, 16, 128, dtype=dtype, device="cuda")
+        big[far] = x
+        pools.append(big)
+    d["kp"], d["vp"] = pools
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + (pages - n), d["table"])
+    out, lse = decode(cuda_lib, w, d, 0, fp32_out=True)
+    w.check_decode(out, lse, 0)
+    w.check_pool(pools[0][far], pools[1][far])
+    again = Paged([200, 31, 77], new=[5, 0, 20], H=8, Hk=2, P=16, dtype=dtype, seed=49)
+    e = again.dev()
+    m = again.kp.shape[0]
+    assert m < n + 20
+    far = torch.arange(pages - m, pages, device="cuda")
+    pools[0][far], pools[1][far] = e["kp"], e["vp"]
+    e["kp"], e["vp"] = pools
+    e["table"] = torch.where(e["table"] >= 0, e["table"] + (pages - m), e["table"])
+    append(cuda_lib, again, e)
+    again.check_pool(pools[0][far], pools[1][far])
+
+
 def test_rows_not_in_use_stay_as_they_were(cuda_lib):
     w = Paged([-1, 37, -1, 0, -1], P=16, seed=13)
     d = w.dev()
