@@ -18,8 +18,6 @@
 
 namespace flint {
 
-constexpr int kCacheBf16 = FLINT_CACHE_BF16, kCacheE4m3 = FLINT_CACHE_E4M3;
-
 // A validated flint_paged_cache_t with its device pointers.
 struct PagedCache {
   int num_pages, P, max_pages, Hk, e4m3;
