@@ -38,9 +38,11 @@
 //     8-15 of one A operand, so q keeps 16 bits of mantissa (22 over e4m3, whose
 //     products run in fp16) and the LSE stays exact to ~1e-6. O^T += V^T P^T has
 //     the heads as the MMA's N, and the P fragment that a lane holds is already
-//     the B operand. P enters that product as fp16 over e4m3 and as a hi and a lo
-//     bf16 part over bf16 (with one part, 2^-8 of each weight, the error of a bf16
-//     output rose by 1.4; the second product took 1% longer); the row sums add the
+//     the B operand. P enters that product as a hi and a lo part as well (fp16 over
+//     e4m3, bf16 over bf16): with one part the output was off by 2.0e-4 over e4m3
+//     (64 sequences, window 4096, root mean square against 64 bits), with two by
+//     1e-6, and the call took 54.3 us for 53.1; over bf16 the error of a bf16 output
+//     rose by 1.4 with one part, and the second took 1% longer. The row sums add the
 //     unrounded values. Over e4m3 the bytes become fp16 in registers (exact), and
 //     the scales multiply S and O in FP32.
 //   * The new token never goes through the cache: its score is formed from the
@@ -710,7 +712,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
               }
             }
         }
-        uint32_t pb[4], pl[4];                                 // P, and over bf16 what it leaves
+        uint32_t pb[4], pl[4];                                 // P's hi and lo parts
         {
           float mx = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));
           mx = fmaxf(mx, fmaxf(fmaxf(sc[2][0], sc[2][1]), fmaxf(sc[3][0], sc[3][1])));
@@ -738,8 +740,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           for (int nt = 0; nt < 4; ++nt) {
             const float p0 = ex2_approx(sc[nt][0] - mb), p1 = ex2_approx(sc[nt][1] - mb);
             sum[nt] = p0 + p1;
-            if constexpr (kF8) pb[nt] = pack_f16x2(p0, p1);
-            else split_pair<false>(p0, p1, pb[nt], pl[nt]);
+            split_pair<kF8>(p0, p1, pb[nt], pl[nt]);
           }
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
@@ -754,17 +755,19 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
             for (int i = 0; i < 4; ++i) {
               uint32_t r[4];
               ldsm_x4<true>(row + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4), r);
+              uint4 av[2];
 #pragma unroll
               for (int d = 0; d < 2; ++d) {
-                uint4 av;
-                e4m3x4_to_f16(__byte_perm(r[2 * d], 0, 0x3120), av.x, av.y);
-                e4m3x4_to_f16(__byte_perm(r[2 * d + 1], 0, 0x3120), av.z, av.w);
+                e4m3x4_to_f16(__byte_perm(r[2 * d], 0, 0x3120), av[d].x, av[d].y);
+                e4m3x4_to_f16(__byte_perm(r[2 * d + 1], 0, 0x3120), av[d].z, av[d].w);
                 if (edge) {
-                  av.x &= vm[2 * c]; av.y &= vm[2 * c];
-                  av.z &= vm[2 * c + 1]; av.w &= vm[2 * c + 1];
+                  av[d].x &= vm[2 * c]; av[d].y &= vm[2 * c];
+                  av[d].z &= vm[2 * c + 1]; av[d].w &= vm[2 * c + 1];
                 }
-                mma16816<kF8>(o[2 * i + d], av, pb[2 * c], pb[2 * c + 1]);
+                mma16816<kF8>(o[2 * i + d], av[d], pb[2 * c], pb[2 * c + 1]);
               }
+              mma16816<kF8>(o[2 * i], av[0], pl[2 * c], pl[2 * c + 1]);
+              mma16816<kF8>(o[2 * i + 1], av[1], pl[2 * c], pl[2 * c + 1]);
             }
           } else {
             const uint32_t row = vst + chunk_at[c] + ((lane & 7) + ((lane >> 4) & 1) * 8) * 128;
