@@ -348,9 +348,7 @@ size_t flint_attn_decode_paged_workspace_bytes(const flint_decode_paged_params_t
 /* flint_attn_decode over a paged cache. Sequence b has p = cache_lens[b] tokens
  * cached; k_hat and v of the new token go into slot p as in
  * flint_attn_paged_append, and the new query sees positions max(0, p-W+1) .. p
- * (as the cache stores them, the new one included) plus the sink. Over e4m3
- * caches softmax_scale * log2(e) * q_hat must stay below 65504 (larger values
- * saturate).
+ * (as the cache stores them, the new one included) plus the sink.
  *   q [B, H, D], k, v [B, Hk, D] bfloat16 (raw projections); q_norm_w, k_norm_w
  *   [D] bfloat16; sink [H] fp32; out [B, H, D] (bf16, or float32 with fp32_out);
  *   lse [B, H] fp32 (natural log).

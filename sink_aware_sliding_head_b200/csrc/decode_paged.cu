@@ -36,7 +36,7 @@
 //     byte the tensor pipe is a fifth busy, and the heads are too few rows for a
 //     tcgen05 tile. S takes q as two 16-bit parts, hi in rows 0-7 and lo in rows
 //     8-15 of one A operand, so q keeps 16 bits of mantissa (22 over e4m3, whose
-//     products run in fp16) and the LSE stays exact to ~1e-6. O^T += V^T P^T has
+//     products run in fp16 on a q that a power of two lifts) and the LSE stays exact to ~1e-6. O^T += V^T P^T has
 //     the heads as the MMA's N, and the P fragment that a lane holds is already
 //     the B operand. P enters that product as a hi and a lo part as well (fp16 over
 //     e4m3, bf16 over bf16): with one part the output was off by 2.0e-4 over e4m3
@@ -78,7 +78,8 @@ constexpr float kRescale = 8.0f;             // log2 units
 template <int NG>
 struct __align__(16) Seg {
   // A operand of S, 8 heads and 16 channels each: rows 0-7 the hi parts, rows
-  // 8-15 the lo parts of the heads' q_hat (log2 units), as the lanes hold it
+  // 8-15 the lo parts of the heads' q_hat, as the lanes hold it; times scale * log2(e)
+  // over bf16, times q_lift over e4m3 (where ks brings S to log2 units)
   uint4 frag[NG * 8 * 32];
   float vnew[kHeadDim];                      // the new value as the cache stores it, times scale
   RowBits kbits[16], vbits[16];              // the new row as the cache stores it, by lane
@@ -248,12 +249,10 @@ __device__ __forceinline__ void e4m3x4_to_f16(uint32_t x, uint32_t& lo, uint32_t
       "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
       : "=r"(lo), "=r"(hi) : "r"(x));
 }
-// A 16-bit pair's hi part and the part left over.
+// A 16-bit pair's hi part and the part left over (fp16: |x| below 65504).
 template <bool kF8>
 __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   if constexpr (kF8) {
-    x0 = sat_f16(x0);
-    x1 = sat_f16(x1);
     const __half2 h = __floats2half2_rn(x0, x1);
     hi = *reinterpret_cast<const uint32_t*>(&h);
     lo = pack_f16x2(x0 - __low2float(h), x1 - __high2float(h));
@@ -261,6 +260,30 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& hi, uin
     hi = pack_bf16x2(x0, x1);
     lo = pack_bf16x2(x0 - __uint_as_float(hi << 16), x1 - __uint_as_float(hi & 0xffff0000u));
   }
+}
+
+// Over e4m3 q enters S in fp16, whose steps stop shrinking at 2^-24: it is lifted by
+// the power of two 2^(11 - k), max|w_q| in 2^k .. 2^(k+1). |q_hat| <= sqrt(128) max|w_q|
+// then lies below 2^15.6 (fp16 ends at 65504), and its two parts are off by 2^-22 of a
+// channel or 2^-36 max|w_q|, whatever the weights, the cache's scales and softmax_scale
+// (unlifted, weights of 2^-10 against key scales of 2^10 times the usual put the LSE off
+// by 3e-5, and 2^-20 by 3e-2). Every lane of the half-warp gets it.
+__device__ __forceinline__ float q_lift(const RowPart& w) {
+  float m = 0.f;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    float x[4];
+    w.get(h, x);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) m = fmaxf(m, fabsf(x[e]));
+  }
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const int exponent = 127 + 11 - ((__float_as_int(m) >> 23) - 127);
+  return __int_as_float(min(max(exponent, 2), 252) << 23);   // its inverse is normal, too
+}
+__device__ __forceinline__ float inverse_of_power(float p) {
+  return __int_as_float((254 << 23) - __float_as_int(p));
 }
 
 // Channels d .. d+3 of an output row from the joined sums, and its LSE once.
@@ -482,6 +505,10 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     constexpr int kHw = 2 * kRowWarps, kRows = 8 * NG / kHw;   // rows of a half-warp: hw + kHw i
     const bool lead = warp == kMathWarps;
     const RowPart wq = unpack_row(load_row(a.wq)), wk = unpack_row(load_row(a.wk));
+    const float lift = kF8 ? q_lift(wq) : A.scale_log2;        // what q is multiplied by
+    auto to_log2 = [&](float x) {                              // what is left to log2 units
+      return kF8 ? x * (inverse_of_power(lift) * A.scale_log2) : x;
+    };
     Angles angles{};
     double f[4];
 #pragma unroll
@@ -557,14 +584,14 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           kn.get(h2, kh);
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            xs[h2][e] = r < a.G ? xs[h2][e] * A.scale_log2 : 0.f;   // zero past G
+            xs[h2][e] = r < a.G ? xs[h2][e] * lift : 0.f;      // zero past G
             z += xs[h2][e] * kh[e];
           }
         }
         if (owner) {                                           // the new token's score
 #pragma unroll
           for (int o = 8; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-          if (l16 == 0) sg.snew[r] = z;
+          if (l16 == 0) sg.snew[r] = to_log2(z);
         }
         // The lane's channels 4 l16 .. are a quarter of chunk l16 / 4 (and of chunk
         // l16 / 4 + 4). bf16: the lanes of head r (4 r + tig) hold channels 2 tig,
@@ -587,7 +614,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       if (lead && lane < 16) sg.sink[lane] = cur.sink;
       if (lead && lane == 0) {
-        sg.ks = cur.ks;
+        sg.ks = to_log2(cur.ks);
         sg.vs = cur.vs;
         sg.dst = (unsigned)cur.page < (unsigned)a.c.num_pages
                      ? cur.page * a.c.page_stride + cur.slot * a.c.token_stride : -1;

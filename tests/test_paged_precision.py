@@ -33,3 +33,12 @@ def test_two_parts_pass_and_one_part_of_either_fails(dtype):
     assert lse > 4 and out > 4
     lse, out = emulate(dtype, 2, 1)
     assert lse < 0.5 and out > 4
+
+
+@pytest.mark.parametrize("small", [2.0 ** -10, 2.0 ** -20])
+def test_small_q_in_fp16_fails_unless_lifted(small):
+    """fp16 parts of a q that is small (against large key scales): steps of 2^-24 at the least.
+    Unlifted, what is rounded is q in log2 units."""
+    assert emulate(E4M3, 2, 2, small, 128 ** -0.5 * np.log2(np.e))[0] > 4
+    lift = 2.0 ** (11 - np.floor(np.log2(small)))
+    assert max(emulate(E4M3, 2, 2, small, lift)) < 0.5

@@ -20,3 +20,41 @@ def test_output_and_lse_keep_two_parts_of_each_operand(cuda_lib, H, Hk, W, rope,
     d = w.dev()
     out, lse = decode(cuda_lib, w, d, W, fp32_out=True)
     pp.check(w, out, lse, d["kp"], d["vp"], W)
+
+
+@pytest.mark.parametrize("softmax_scale", [False, True])
+@pytest.mark.parametrize("power", [-20, -10, 8, 20])
+def test_q_of_any_size_over_e4m3(cuda_lib, power, softmax_scale):
+    """Norm weights (or a softmax scale) and key scales whose powers of two cancel: the scores
+    are of the usual size, q is not."""
+    lens = np.random.RandomState(7).randint(0, 130, 40).tolist()
+    w = Paged(lens, H=16, Hk=2, P=16, dtype=E4M3, seed=62)
+    w.k_scale = w.k_scale * 2.0 ** -power
+    w.wk = w.wk * 2.0 ** -power
+    scale = 128 ** -0.5
+    if softmax_scale:
+        scale = scale * 2.0 ** power
+    else:
+        w.wq = w.wq * 2.0 ** power
+    d = w.dev()
+    out, lse = decode(cuda_lib, w, d, 0, fp32_out=True, softmax_scale=scale)
+    pp.check(w, out, lse, d["kp"], d["vp"], 0, scale)
+
+
+def test_weights_of_q_that_differ_by_channel(cuda_lib):
+    """q's small channels meet large keys, over e4m3."""
+    w = Paged([0, 9, 65, 100] * 10, H=16, Hk=2, P=16, dtype=E4M3, rope=False, seed=63)
+    ramp = 2.0 ** -torch.arange(128).remainder(8).float()      # 1 to 2^-7
+    w.wq = (w.wq.float() * ramp).to(BF16)
+    d = w.dev()
+    out, lse = decode(cuda_lib, w, d, 0, fp32_out=True)
+    pp.check(w, out, lse, d["kp"], d["vp"], 0)
+
+
+def test_zero_weights_of_q(cuda_lib):
+    """All scores are zero: nothing to lift, the weights are equal."""
+    w = Paged([0, 1, 70], H=8, Hk=2, P=16, dtype=E4M3, seed=64)
+    w.wq = torch.zeros_like(w.wq)
+    d = w.dev()
+    out, lse = decode(cuda_lib, w, d, 0, fp32_out=True)
+    pp.check(w, out, lse, d["kp"], d["vp"], 0)
