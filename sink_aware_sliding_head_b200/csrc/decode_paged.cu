@@ -186,7 +186,7 @@ struct Walk {
       off = 0;
       do {                                   // ends: left > 0 units lie in later rows
         ++b;
-        r = row_range(a, b - b0 < kLensKept ? lens[b - b0] : __ldg(a.lens + b));
+        r = row_range(a, b - b0 < kLensKept ? lens[b - b0] : load(a.lens + b));
       } while (r.n == 0);
     }
     return cut();
@@ -340,7 +340,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     // (those take as long as one: 230 keys took 9.5 us in four ranges a pair and
     // a join, 7.2 in one); the cost fills up a pair's last range.
     w.b = w.b0 = 0;
-    w.r = row_range(a, __ldg(a.lens));
+    w.r = row_range(a, load(a.lens));
     __syncthreads();
     const int n = w.r.n, most = (int)gridDim.x / a.c.Hk;
     if (n == 0) {
@@ -368,7 +368,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const int b0 = min(a.B, (int)threadIdx.x * per), b1 = min(a.B, b0 + per);
     long long sum = 0;
     for (int b = b0; b < b1; ++b) {
-      const int p = __ldg(a.lens + b);
+      const int p = load(a.lens + b);
       const Range r = row_range(a, p);
       if (a.B <= kLensKept) sm.lens[b] = p;
       sum += r.n ? w.cost + r.n : 0;
@@ -397,7 +397,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     if (at >= 0 && at < sum * a.c.Hk) {
       int b = b0;
       for (;; ++b) {                         // ends inside b0 .. b1-1: at < sum * Hk
-        const int n = row_range(a, a.B <= kLensKept ? sm.lens[b] : __ldg(a.lens + b)).n;
+        const int n = row_range(a, a.B <= kLensKept ? sm.lens[b] : load(a.lens + b)).n;
         const long long units_b = n ? (long long)(w.cost + n) * a.c.Hk : 0;
         if (at < units_b) break;
         at -= units_b;
@@ -408,7 +408,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     __syncthreads();
     if (a.B > kLensKept) {                   // the rows from the range's first
       for (int i = threadIdx.x; i < min(kLensKept, a.B - sm.start_b); i += kThreads)
-        sm.lens[i] = __ldg(a.lens + sm.start_b + i);
+        sm.lens[i] = load(a.lens + sm.start_b + i);
       __syncthreads();
     }
     w.b = sm.start_b;
@@ -435,7 +435,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       const bool need = i < v.len * nbox && pos + A.box > v.r.lo && pos < v.r.p;
       const int col = page_col(A, pos);
       const int32_t* row = a.c.table + v.b * a.c.table_stride;
-      return Box{need ? max(__ldg(row + col), -1) : -2, pos - col * a.c.P};
+      return Box{need ? max(load(row + col), -1) : -2, pos - col * a.c.P};
     };
     Box next = fetch(w, 0);
     while (true) {
@@ -526,11 +526,11 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       h.k = load_row(a.k + v.b * a.k_stride + v.g * kHeadDim);
       h.v = load_row(a.v + v.b * a.v_stride + v.g * kHeadDim);
       const int col = page_col(A, v.r.p);
-      h.page = __ldg(a.c.table + v.b * a.c.table_stride + col);
+      h.page = load(a.c.table + v.b * a.c.table_stride + col);
       h.slot = v.r.p - col * a.c.P;
-      h.sink = lane < a.G ? __ldg(a.sink + v.g * a.G + lane) : 0.f;
-      h.ks = kF8 && a.c.k_scale ? __ldg(a.c.k_scale + v.g) : 1.f;
-      h.vs = kF8 && a.c.v_scale ? __ldg(a.c.v_scale + v.g) : 1.f;
+      h.sink = lane < a.G ? load(a.sink + v.g * a.G + lane) : 0.f;
+      h.ks = kF8 && a.c.k_scale ? load(a.c.k_scale + v.g) : 1.f;
+      h.vs = kF8 && a.c.v_scale ? load(a.c.v_scale + v.g) : 1.f;
       return h;
     };
     Raw h = look(w);
@@ -932,7 +932,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   const int part_warps = both ? kMathWarps / 2 : kMathWarps;
   const Part q = (both ? warp >= part_warps : sm.last[1]) ? last_part : first_part;
   for (int r = warp % part_warps; r < a.G; r += part_warps) {
-    float M = __ldg(a.sink + q.g * a.G + r) * kLog2e, L = 1.f;   // the sink first, then in order
+    float M = load(a.sink + q.g * a.G + r) * kLog2e, L = 1.f;   // the sink first, then in order
     float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int c = q.c0; c <= q.c1; c += 32) {
       const int n = min(32, q.c1 - c + 1);

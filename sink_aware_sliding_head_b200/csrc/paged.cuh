@@ -18,6 +18,13 @@
 
 namespace flint {
 
+// Lengths, tables and scales may have been written by the kernel before this one, whose
+// end these kernels may overlap (previous_done). So they are read by ordinary loads: the
+// read-only path (__ldg) is for memory that nobody writes while the kernel lives, and its
+// loads may be moved to before the wait.
+template <typename T>
+__device__ __forceinline__ T load(const T* p) { return *p; }
+
 // A validated flint_paged_cache_t with its device pointers.
 struct PagedCache {
   int num_pages, P, max_pages, Hk, e4m3;
@@ -32,7 +39,7 @@ struct PagedCache {
 __device__ __forceinline__ long long slot_offset(const PagedCache& c, int b, int pos) {
   const int col = pos / c.P;
   if (pos < 0 || col >= c.max_pages) return -1;
-  const int page = __ldg(c.table + b * c.table_stride + col);
+  const int page = load(c.table + b * c.table_stride + col);
   if ((unsigned)page >= (unsigned)c.num_pages) return -1;
   return page * c.page_stride + (pos - col * c.P) * c.token_stride;
 }
@@ -140,7 +147,7 @@ __device__ __forceinline__ void row_prologue(RowPart& r, const RowPart& w, const
 // (16 divisions a lane cost as much as the rest of the row).
 __device__ __forceinline__ float inv_scale(const float* scale, int g) {
   float r = 1.f;
-  if (scale) asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(__ldg(scale + g)));
+  if (scale) asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(load(scale + g)));
   return r;
 }
 __device__ __forceinline__ uint32_t f2_to_bf16x2(uint64_t v) {

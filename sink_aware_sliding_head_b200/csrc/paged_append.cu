@@ -37,6 +37,16 @@ constexpr int blocks_per_sm(int heads) {
   return heads <= 2 ? 8 : heads == 4 ? 5 : 4;
 }
 
+// The sequence of token t: the last b with cu[b] <= t, so that none is empty.
+__device__ __forceinline__ int seq_of(const int32_t* cu, int N, int t) {
+  int lo = 0, hi = N;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (load(cu + mid) <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
 template <bool kE4m3, int kHeads>
 __global__ void __launch_bounds__(kThreads, blocks_per_sm(kHeads))
 paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
@@ -46,7 +56,7 @@ paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
   double f[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) f[e] = rope_turns(4 * l + e, a.rope_pow);
-  const int used = min(a.T, __ldg(a.cu + a.N));      // tokens past the last sequence: none
+  const int used = min(a.T, load(a.cu + a.N));      // tokens past the last sequence: none
   const long long step = (long long)gridDim.x * (kThreads / 16);
   const long long first = (long long)blockIdx.x * (kThreads / 16) + (threadIdx.x >> 4);
   // Both half-warps of a warp take as many turns: the shuffles are the warp's.
@@ -68,8 +78,8 @@ paged_append_kernel(const __grid_constant__ PagedAppendLaunch a) {
     long long off = -1;                              // the token's slot, -1: none
     int pos = 0;
     if (live) {
-      const int b = doc_of(a.cu, a.N, (int)t), len = __ldg(a.lens + b);
-      const long long p = len + t - __ldg(a.cu + b);
+      const int b = seq_of(a.cu, a.N, (int)t), len = load(a.lens + b);
+      const long long p = len + t - load(a.cu + b);
       if (len >= 0 && p >= 0 && p < (long long)a.c.P * a.c.max_pages) {
         pos = (int)p;
         off = slot_offset(a.c, b, pos);
