@@ -88,3 +88,46 @@ def test_steps_back_to_back_are_the_steps_one_by_one(cuda_lib, dtype):
 
     for a, b in zip(loop(True), loop(False)):
         assert torch.equal(a, b)
+
+
+@pytest.mark.gpu
+def test_captured_behind_copies_fills_and_joined_streams(cuda_lib):
+    """In a captured step the paged calls follow copies, fills and a second stream, not only
+    kernels of their own stream."""
+    fa = cuda_lib
+    w = Paged([70, 3, 200], H=16, Hk=2, P=16, seed=72)
+    d = w.dev()
+    kp0, vp0 = d["kp"].clone(), d["vp"].clone()
+    host = torch.tensor(w.lens, dtype=torch.int32).pin_memory()
+    lens = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    lens2 = torch.full((3,), -1, dtype=torch.int32, device="cuda")
+    status = torch.ones(64, dtype=torch.int32, device="cuda")
+    out, lse = torch.zeros(3, 16, D, device="cuda"), torch.zeros(3, 16, device="cuda")
+    ws = fa.alloc_decode_paged_workspace(3, 16, 2)
+    side = torch.cuda.Stream()
+    args = d["k"], d["v"], d["wk"], d["cu"]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            lens2.copy_(host, non_blocking=True)                  # a copy node on the other stream
+            fa.paged_append(*args, lens2, d["table"], d["kp"], d["vp"], w.rope, THETA,
+                            status=torch.zeros(64, dtype=torch.int32, device="cuda"))
+        status.zero_()
+        lens.copy_(host, non_blocking=True)
+        torch.cuda.current_stream().wait_stream(side)
+        fa.paged_append(*args, lens, d["table"], d["kp"], d["vp"], w.rope, THETA, status=status)
+        lens.copy_(host, non_blocking=True)
+        fa.decode_paged(d["q"], d["k"], d["v"], d["wq"], d["wk"], d["sink"], lens, d["table"],
+                        d["kp"], d["vp"], 0, w.rope, THETA, out=out, lse=lse, fp32_out=True,
+                        workspace=ws)
+        lens.fill_(-1)
+    for _ in range(3):
+        d["kp"].copy_(kp0)
+        d["vp"].copy_(vp0)
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        w.check_decode(out, lse, 0)
+        w.check_pool(d["kp"], d["vp"])
+        assert status[0].item() == 0
