@@ -772,16 +772,22 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
         }
         const uint32_t vst = ring + s * C::kStageBytes + v_at;
+        // The products of the block's 32 keys are summed on their own, then added to O: an
+        // MMA cuts its sum off, toward zero, and a running O would be cut at every step. A
+        // whole pair of 131072 keys in one range, values around one: O 8.2e-5 too small that
+        // way, now within 2e-7; 64 rows of 4096 keys 89.1 us for 88.7, over e4m3 56.8 for
+        // 54.5, 201 ragged rows with nine heads 43.3 for 41.1.
+        if constexpr (kF8) {
+          // ldmatrix on byte pairs: a lane gets channels 2 gid, 2 gid + 1 of keys
+          // 2 tig, 2 tig + 1; rows gid and gid + 8 of the m-tile are those channels
+          const uint32_t row = vst + ((lane & 7) + ((lane >> 3) & 1) * 8) * 128;
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {                          // 16 keys
-          if constexpr (kF8) {
-            // ldmatrix on byte pairs: a lane gets channels 2 gid, 2 gid + 1 of keys
-            // 2 tig, 2 tig + 1; rows gid and gid + 8 of the m-tile are those channels
-            const uint32_t row = vst + chunk_at[c] + ((lane & 7) + ((lane >> 3) & 1) * 8) * 128;
+          for (int i = 0; i < 4; ++i) {
+            float t[2][4] = {};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int c = 0; c < 2; ++c) {                      // 16 keys
               uint32_t r[4];
-              ldsm_x4<true>(row + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4), r);
+              ldsm_x4<true>(row + chunk_at[c] + (((2 * i + (lane >> 4)) ^ (lane & 7)) << 4), r);
               uint4 av[2];
 #pragma unroll
               for (int d = 0; d < 2; ++d) {
@@ -791,26 +797,39 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                   av[d].x &= vm[2 * c]; av[d].y &= vm[2 * c];
                   av[d].z &= vm[2 * c + 1]; av[d].w &= vm[2 * c + 1];
                 }
-                mma16816<kF8>(o[2 * i + d], av[d], pb[2 * c], pb[2 * c + 1]);
+                mma16816<kF8>(t[d], av[d], pb[2 * c], pb[2 * c + 1]);
               }
-              mma16816<kF8>(o[2 * i], av[0], pl[2 * c], pl[2 * c + 1]);
-              mma16816<kF8>(o[2 * i + 1], av[1], pl[2 * c], pl[2 * c + 1]);
-            }
-          } else {
-            const uint32_t row = vst + chunk_at[c] + ((lane & 7) + ((lane >> 4) & 1) * 8) * 128;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
+              for (int d = 0; d < 2; ++d)
+                mma16816<kF8>(t[d], av[d], pl[2 * c], pl[2 * c + 1]);
+            }
+#pragma unroll
+            for (int d = 0; d < 2; ++d)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2)
+                f2_split(fadd2(f2(o[2 * i + d][e], o[2 * i + d][e + 1]), f2(t[d][e], t[d][e + 1])), o[2 * i + d][e], o[2 * i + d][e + 1]);
+          }
+        } else {
+          const uint32_t row = vst + ((lane & 7) + ((lane >> 4) & 1) * 8) * 128;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float t[4] = {};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {                      // 16 keys
               uint32_t r[4];
-              ldsm_x4<true>(row + (i >> 2) * half_bytes +
+              ldsm_x4<true>(row + chunk_at[c] + (i >> 2) * half_bytes +
                                 (((2 * (i & 3) + ((lane >> 3) & 1)) ^ (lane & 7)) << 4), r);
               uint4 av = make_uint4(r[0], r[1], r[2], r[3]);
               if (edge) {
                 av.x &= vm[2 * c]; av.y &= vm[2 * c];
                 av.z &= vm[2 * c + 1]; av.w &= vm[2 * c + 1];
               }
-              mma16816<kF8>(o[i], av, pb[2 * c], pb[2 * c + 1]);
-              mma16816<kF8>(o[i], av, pl[2 * c], pl[2 * c + 1]);
+              mma16816<kF8>(t, av, pb[2 * c], pb[2 * c + 1]);
+              mma16816<kF8>(t, av, pl[2 * c], pl[2 * c + 1]);
             }
+#pragma unroll
+              for (int e = 0; e < 4; e += 2)
+                f2_split(fadd2(f2(o[i][e], o[i][e + 1]), f2(t[e], t[e + 1])), o[i][e], o[i][e + 1]);
           }
         }
       }

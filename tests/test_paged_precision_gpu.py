@@ -58,3 +58,39 @@ def test_zero_weights_of_q(cuda_lib):
     d = w.dev()
     out, lse = decode(cuda_lib, w, d, 0, fp32_out=True)
     pp.check(w, out, lse, d["kp"], d["vp"], 0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, E4M3])
+def test_long_sums_are_not_cut_off(cuda_lib, dtype):
+    """Values around one, 30000 keys in one range of keys: the errors of single keys average out,
+    what is left is what the long sums do. A matrix product's sums are cut off toward zero, some
+    2^-24.5 a step, and a running output would be cut in each of its ~470 steps here (2^-15.7).
+
+    Bound: 2^-17 of each weight (bf16 parts) over 30000 keys of like weights, sqrt(30000) =
+    2^7.4: 2^-24. The roundings in 32 bits that all keys share or that have one sign, twenty of
+    2^-23 at the most: below 2^-18."""
+    Hk, p, P = 148, 30000, 64                     # one row, a range for each of its KV heads
+    n = -(-(p + 1) // P)
+    gen = torch.Generator(device="cuda").manual_seed(65)
+    kp, vp = (torch.empty(n, Hk, P, 128, dtype=dtype, device="cuda") for _ in "kv")
+    for at in range(0, n, 64):
+        shape = kp[at:at + 64].shape
+        kp[at:at + 64] = torch.randn(shape, generator=gen, device="cuda").to(dtype)
+        vp[at:at + 64] = (1 + 0.2 * torch.randn(shape, generator=gen, device="cuda")).to(dtype)
+    table = torch.randperm(n, generator=gen, device="cuda").to(torch.int32)[None]
+    w = Paged([0], H=Hk, Hk=Hk, P=16, rope=False, seed=66)
+    d = w.dev()
+    lens = torch.tensor([p], dtype=torch.int32, device="cuda")
+    d["v"] = torch.ones_like(d["v"])
+    out, _ = cuda_lib.decode_paged(d["q"], d["k"], d["v"], d["wq"], d["wk"], d["sink"], lens,
+                                   table, kp, vp, 0, False, 1e6, check_status=True, fp32_out=True)
+    w.lens = [p]
+    q = torch.as_tensor(pp.fo.prologue(w.q.double().numpy(), w.wq.double().numpy(),
+                                       np.array([p]), False, 1e6, 1e-6)[0]).cuda()
+    errors = []
+    for h in range(Hk):
+        K, V = (x[table[0].long(), h].reshape(-1, 128)[:p + 1].double() for x in (kp, vp))
+        z = torch.cat([K @ q[h] * 128 ** -0.5, d["sink"][h:h + 1].double()])
+        e = torch.softmax(z, 0)[:-1]
+        errors.append((out[0, h].double() - e @ V) / (e @ V.abs()))
+    assert pp.rms(torch.stack(errors).cpu().numpy()) <= 2.0 ** -18
