@@ -70,7 +70,8 @@ def rms(x):
 def off_by(got, want):
     """(rms of the LSE's error, rms of the output's error relative to the weighted |v|)."""
     lse = np.concatenate([g[1] - r[1] for g, r in zip(got, want)])
-    out = np.concatenate([((g[0] - r[0]) / r[2]).ravel() for g, r in zip(got, want)])
+    out = np.concatenate([((g[0] - r[0]) / np.maximum(r[2], 1e-30)).ravel()
+                          for g, r in zip(got, want)])
     return rms(lse), rms(out)
 
 
