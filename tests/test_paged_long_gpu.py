@@ -1,6 +1,6 @@
 """Calls long enough that the paged kernels use everything twice: the decode kernel's ring stages,
 barriers and segment slots in all four variants, and further turns of the append kernel's loop.
-Also e4m3 pools that one tensor map cannot hold together."""
+Also e4m3 pools that one tensor map cannot hold together, and a dense cache as a pool."""
 import numpy as np
 import pytest
 import torch
@@ -91,3 +91,19 @@ def test_keys_and_values_in_one_pool(cuda_lib, P):
         same[int(pg[0]), int(sl[0])] = False
     a, c = (t.cpu().view(torch.uint8).transpose(1, 2)[same] for t in (d["kp"], w.kp))
     assert torch.equal(a, c)
+
+
+def test_a_dense_cache_is_a_pool_of_one_page_to_a_row(cuda_lib):
+    """[B, Hk, C, D] with row b in page b gives the bits that scattered pages of C slots give."""
+    lens = [0, 511, 63, 300]
+    w = Paged(lens, H=16, Hk=2, P=512, seed=84, extra_cols=0)
+    d = w.dev()
+    dense = [t[d["table"][:, 0].long()].contiguous() for t in (d["kp"], d["vp"])]
+    rows = torch.arange(4, device="cuda", dtype=torch.int32)[:, None]
+    out, lse = decode(cuda_lib, w, d, 200, fp32_out=True)
+    w.check_decode(out, lse, 200)
+    scattered = d["table"][:, 0].long()
+    e = dict(d, kp=dense[0], vp=dense[1], table=rows)
+    again = decode(cuda_lib, w, e, 200, fp32_out=True)
+    assert torch.equal(out, again[0]) and torch.equal(lse, again[1])
+    assert torch.equal(dense[0], d["kp"][scattered]) and torch.equal(dense[1], d["vp"][scattered])
