@@ -248,7 +248,10 @@ flint_status_t flint_attn_decode(const flint_decode_params_t* params,
  * on the Flint config page through use_cache; paging is this library's own).
  * flint_attn_paged_append fills the cache (a prompt after flint_attn_fwd, a
  * chunk of one, single tokens, any mix); flint_attn_decode_paged appends one new
- * token per sequence and attends with it.
+ * token per sequence and attends with it. (No call attends with several new tokens
+ * over a cache: the queries of a chunk behind cached tokens need flint_attn_fwd over
+ * the whole prompt.) A dense cache [B, Hk, C, D] with C a multiple of 16 is a pool of
+ * B pages of C slots.
  *
  * Position t of sequence b lives in page block_table[b * table_stride + t / P],
  * slot t % P (P = page_size). KV head g's 128 channels start at element

@@ -7,7 +7,7 @@
 // lens[b], and the new query sees slots max(0, p - W + 1) .. p plus the sink.
 //
 // Bound by HBM: a key costs 512 bytes of K and V (256 in e4m3) and feeds only
-// the G query heads of its group, 2 G operations a byte.
+// the G query heads of its group with 512 G operations: G a byte (2 G in e4m3).
 //
 //   * Work. The keys of all (sequence, KV head) pairs are laid end to end in
 //     blocks of 64 positions, each pair behind a few units of nothing that stand
@@ -25,34 +25,39 @@
 //     that divides the page, at most 64, so no box crosses a page. Issuing a copy
 //     costs a warp 130 cycles or more, so e4m3, whose rows need no halves, takes
 //     that dimension for K and V and copies both at once (64 sequences, window
-//     4096, 16-slot pages: 58.2 us with a copy each, 54.0 with one for both).
-//   * Rows. With the rings of 148 SMs full, 19 MB are in flight and any load
-//     waits ~3 us behind them. Two more warps therefore fetch, normalise and
-//     rotate the q rows and the new row of the coming segments, up to four ahead,
-//     and lay q out as the products take it.
+//     4096, 16-slot pages: 60.3 us with a copy each, 56.1 with one for both).
+//   * Rows. With the rings of 148 SMs full, 24 MB are in flight (19 MB with 9 to 16
+//     heads) and any load waits 3 to 4 us behind them. Two more warps
+//     therefore fetch, normalise and rotate the q rows and the new row of the coming
+//     segments, up to four ahead, and lay q out as the products take it.
 //   * Math. Eight warps take the blocks in turn, 32 keys and eight query heads a
 //     warp (up to 8 heads: four pairs of warps, a block each; 9 to 16: two groups
-//     of four), on mma.sync m16n8k16 with FP32 accumulation: at 2 G operations a
-//     byte the tensor pipe is a fifth busy, and the heads are too few rows for a
-//     tcgen05 tile. S takes q as two 16-bit parts, hi in rows 0-7 and lo in rows
-//     8-15 of one A operand, so q keeps 16 bits of mantissa (22 over e4m3, whose
-//     products run in fp16 on a q that a power of two lifts) and the LSE stays exact to ~1e-6. O^T += V^T P^T has
-//     the heads as the MMA's N, and the P fragment that a lane holds is already
-//     the B operand. P enters that product as a hi and a lo part as well (fp16 over
-//     e4m3, bf16 over bf16): with one part the output was off by 2.0e-4 over e4m3
-//     (64 sequences, window 4096, root mean square against 64 bits), with two by
-//     1e-6, and the call took 54.3 us for 53.1; over bf16 the error of a bf16 output
-//     rose by 1.4 with one part, and the second took 1% longer. The row sums add the
-//     unrounded values. Over e4m3 the bytes become fp16 in registers (exact), and
-//     the scales multiply S and O in FP32.
+//     of four), on mma.sync m16n8k16 with FP32 accumulation: at G or 2 G operations
+//     a byte the tensor pipe is a fifth busy over bf16 and a quarter over e4m3, and
+//     the heads are too few rows for a tcgen05 tile. S takes q as two 16-bit parts,
+//     hi in rows 0-7 and lo in rows 8-15 of one A operand. O^T += V^T P^T has the
+//     heads as the MMA's N, and the P fragment that a lane holds is already the B
+//     operand; P is a hi and a lo part as well. The row sums add the unrounded
+//     values. Over e4m3 the bytes become fp16 in registers (exact), q and P are fp16,
+//     and the scales multiply S and O in FP32.
+//   * Precision. Two parts are 16 bits of q and P over bf16 and 22 over e4m3 (a power
+//     of two lifts q there). A score is off by at most 2^-17 scale sum |q_i K_i| over
+//     bf16 and 2^-22 over e4m3, beside FP32's own. Against 64 bits, with a float32
+//     output (64 sequences, window 4096): the output by 3.9e-6 of its size over bf16
+//     and 2.8e-7 over e4m3, the LSE by 6e-7 and 4e-7 (root mean squares; at most 2e-6
+//     and 1e-6). With one part of P it was 2.0e-4 over e4m3 (and the kernel 2% faster),
+//     and the error of a bf16 output rose by 1.4 over bf16. A third part of q and of P
+//     over bf16 would be 1.9e-6 at 94.3 us for 89.6 and, with nine heads to a KV head,
+//     56 us for 43: not taken, a bf16 output rounds by 1.7e-3.
 //   * The new token never goes through the cache: its score is formed from the
 //     rounded row and enters when the warps of its segment are joined. Its row
 //     is stored after the segment's last load has landed.
 //
 // Measured (B200, 6.56 TB/s copy): 64 sequences of 4096 visible keys, 32 query and
-// 4 KV heads, 89 us in bf16 (6.0 TB/s), 53 us in e4m3 (5.1 TB/s); four sequences
-// near 131072 keys 141 us (6.7 TB/s); one row of 230 keys 6.1 us. The fixed part is
-// ~5 us: the plan, the first rows and pages (each a trip to HBM), and the join.
+// 4 KV heads, 89 us in bf16 (6.0 TB/s), 56 us in e4m3 (4.8 TB/s); four sequences
+// near 131072 keys 142 us (6.6 TB/s; 154 on a slower card); one row of 230 keys 6.2 to
+// 6.5 us. The fixed part is ~5 us: the plan, the first rows and pages (each a trip to
+// HBM), and the join.
 #include "paged.cuh"
 #include "sm100_primitives.cuh"
 
@@ -107,8 +112,9 @@ struct Cfg {
   static constexpr int kRowBytes = kF8 ? kHeadDim : 2 * kHeadDim;
   static constexpr int kStageBytes = 2 * kBlk * kRowBytes;          // boxes of K and V rows
   // A pair's fixed cost in units. 201 rows of up to 2513 keys, nine heads to a KV
-  // head, cost 0, 4, 8, 12: 54.1, 43.8, 44.8, - us in bf16, 58.4, 45.8, 44.9, 46.3
-  // in e4m3; 250 rows of up to 900: 71.8, 53.2, 54.2, - and 76.0, 53.1, 47.5, 47.3.
+  // head, cost 0, 4, 8, 12: 49.3, 43.0, 44.9, 46.2 us in bf16, 51.0, 43.2, 45.3, 46.7
+  // in e4m3; 250 rows of up to 900, eight heads: 73.4, 51.1, 53.2, 55.3 in bf16, 75.8,
+  // 45.7, 45.4, 46.6 in e4m3 (whose blocks have half the bytes; 4 would do there, too).
   static constexpr int kCost = kF8 ? 8 : 4;
   static constexpr int kGroupWarps = 2 * NG, kGroups = kMathWarps / kGroupWarps;
   // Block u goes to stage u % kStages, to group u % kGroups, and has the barriers
@@ -232,6 +238,11 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint4 a, uint32_t 
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void add4(float (&x)[4], const float (&y)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; e += 2)
+    f2_split(fadd2(f2(x[e], x[e + 1]), f2(y[e], y[e + 1])), x[e], x[e + 1]);
+}
 template <bool kTrans>
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
   if constexpr (kTrans)
@@ -337,8 +348,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
   if (a.B == 1) {
     // One row's pairs are all alike: each gets ranges of its own, as many as
     // there are SMs for, but not below a block for each group of math warps
-    // (those take as long as one: 230 keys took 9.5 us in four ranges a pair and
-    // a join, 7.2 in one); the cost fills up a pair's last range.
+    // (those take as long as one: 230 keys take 8.7 us in four ranges a pair and
+    // a join, 6.5 in one); the cost fills up a pair's first range.
     w.b = w.b0 = 0;
     w.r = row_range(a, load(a.lens));
     __syncthreads();
@@ -804,10 +815,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
                 mma16816<kF8>(t[d], av[d], pl[2 * c], pl[2 * c + 1]);
             }
 #pragma unroll
-            for (int d = 0; d < 2; ++d)
-#pragma unroll
-              for (int e = 0; e < 4; e += 2)
-                f2_split(fadd2(f2(o[2 * i + d][e], o[2 * i + d][e + 1]), f2(t[d][e], t[d][e + 1])), o[2 * i + d][e], o[2 * i + d][e + 1]);
+            for (int d = 0; d < 2; ++d) add4(o[2 * i + d], t[d]);
           }
         } else {
           const uint32_t row = vst + ((lane & 7) + ((lane >> 4) & 1) * 8) * 128;
@@ -827,9 +835,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
               mma16816<kF8>(t, av, pb[2 * c], pb[2 * c + 1]);
               mma16816<kF8>(t, av, pl[2 * c], pl[2 * c + 1]);
             }
-#pragma unroll
-              for (int e = 0; e < 4; e += 2)
-                f2_split(fadd2(f2(o[i][e], o[i][e + 1]), f2(t[e], t[e + 1])), o[i][e], o[i][e + 1]);
+            add4(o[i], t);
           }
         }
       }

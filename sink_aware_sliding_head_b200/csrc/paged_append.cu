@@ -13,12 +13,12 @@
 // shared memory nor a barrier. Blocks are persistent, so a lane forms its four
 // frequencies once.
 //
-// Measured (B200, 6.56 TB/s copy): 65536 prompt tokens of 4 KV heads 46 us (5.8
-// TB/s), 131072 without RoPE 88 us (6.1 TB/s); 22539 tokens of 8 heads to e4m3 32 us
-// (4.4 TB/s: the instructions of the conversions and waits for loads bound it).
-// Requesting the next token's rows before the current one's are done was slower
-// (65536 tokens: 55 us), and so were four tokens a half-warp at a time where there
-// is one KV head (65536 tokens: 25.3 us with one, 26.1 with four).
+// Measured (B200, 6.56 TB/s copy): 65536 prompt tokens of 4 KV heads 45 us (5.9
+// TB/s), 131072 without RoPE 87 us (6.2 TB/s); 22539 tokens of 8 heads to e4m3 30 us
+// (4.6 TB/s: half of the issue slots and 40% of HBM are used; 16 warps an SM overlap
+// their loads and conversions too little). Requesting the next token's rows before the
+// current one's are done was slower when tried (65536 tokens: 55 us for 48), and so
+// were four tokens a half-warp at a time where there is one KV head (25.3, 26.1).
 #include "paged.cuh"
 
 namespace flint {
@@ -28,11 +28,12 @@ namespace {
 constexpr int kThreads = 128;                // 8 tokens at a time
 
 // Heads whose rows are in flight together (four loads of 8 bytes a lane each), and
-// blocks per SM by the registers that takes. Eight heads in two turns of 4 against
-// one of 8 took 53.4 and 46.4 us (32000 tokens, bf16), 37.1 and 31.7 (22539 to
-// e4m3); four heads in a turn of 4 or half a turn of 8 46.2 and 47.9 us (65536
-// tokens, bf16); one head in a quarter of a turn of 4 or a turn of its own 25.2 and
-// 21.3, two 31.2 and 27.0.
+// blocks per SM by the registers that takes (two heads: 64 registers, 24 bytes of a
+// lane's state in memory in bf16, 8 in e4m3). Eight heads in two turns of 4 against one
+// of 8 take 53.9 and 45.8 us (32768 tokens, bf16), 49.8 and 41.3 (to e4m3); four heads in
+// a turn of 4 or half a turn of 8 45.0 and 46.7, 44.7 and 47.4 (65536 tokens); one head in
+// a turn of its own or a quarter of one of 4 20.6 and 23.7, 22.8 and 24.8; two heads 26.9
+// and 30.7, 30.2 and 30.9.
 constexpr int blocks_per_sm(int heads) {
   return heads <= 2 ? 8 : heads == 4 ? 5 : 4;
 }
@@ -119,11 +120,14 @@ cudaError_t launch_paged_append(const PagedAppendLaunch& a, int num_sms, cudaStr
   ProfScope prof(kKPagedAppend, st);
   const int per = kThreads / 16;
   const int blocks = (int)(((long long)a.T + per - 1) / per);
-  // bf16, bound by HBM: four times the resident blocks, which even out the SMs
-  // (131072 tokens: 96.7 us with one, 88.2 with four, 83.4 with all; 65536 of one
-  // KV head, four in flight, 24.2, 25.4, 28.3: every block forms its frequencies).
-  // e4m3 is bound by its instructions: one (22539 tokens, four heads in flight,
-  // 36.6 us, with four 39.3).
+  // A grid of 1, 2 or 4 times the resident blocks, or of all (16 sequences, RoPE). More
+  // blocks even out the SMs; every block forms its frequencies anew.
+  //   bf16  262144 tokens of 1 head 76.7, 73.1, 71.0, 82.8 us; 131072 of 2 50.0, 48.5,
+  //         48.3, 52.5; 65536 of 4 46.2, 45.7, 45.1, 46.6; 32768 of 8 49.5, 48.0, 45.6, 45.1
+  //   e4m3  83.7, 79.0, 76.8, 88.5; 57.8, 54.1, 53.5, 57.8; 44.5, 44.0, 44.2, 47.1; 42.0,
+  //         43.1, 42.7, 43.3
+  // bf16 takes four times, e4m3 once: best with eight heads, as good with four, 8% slower
+  // than four times with one or two.
   typedef void (*Kernel)(PagedAppendLaunch);
   static const Kernel kernels[2][4] = {
       {paged_append_kernel<false, 1>, paged_append_kernel<false, 2>,
