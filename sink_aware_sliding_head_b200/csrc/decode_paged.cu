@@ -517,9 +517,6 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
     const bool lead = warp == kMathWarps;
     const RowPart wq = unpack_row(load_row(a.wq)), wk = unpack_row(load_row(a.wk));
     const float lift = kF8 ? q_lift(wq) : A.scale_log2;        // what q is multiplied by
-    auto to_log2 = [&](float x) {                              // what is left to log2 units
-      return kF8 ? x * (inverse_of_power(lift) * A.scale_log2) : x;
-    };
     Angles angles{};
     double f[4];
 #pragma unroll
@@ -558,6 +555,8 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
           !mbar_wait_warp(smem_u32(&sm.seg_empty[k % kSegs]), (k / kSegs - 1) & 1, wc))
         break;
       const bool owner = w.blk + w.len == w.r.n;
+      // what brings a product of the lifted q and a stored key to log2 units
+      const float s_scale = kF8 ? cur.ks * (inverse_of_power(lift) * A.scale_log2) : 1.f;
       RowPart kn{};                                            // as the cache stores it
       if (owner) {                                             // every half-warp the same row
         kn = unpack_row(cur.k);
@@ -567,7 +566,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         if constexpr (kF8) {
           kb = pack_e4m3(kn, inv_scale(a.c.k_scale, w.g));
           vb = pack_e4m3(vn, inv_scale(a.c.v_scale, w.g));
-          kn = unpack_e4m3(kb, cur.ks);
+          kn = unpack_e4m3(kb, 1.f);                           // its scale goes into s_scale
           vn = unpack_e4m3(vb, cur.vs);
         } else {
           kb = pack_bf16(kn);
@@ -602,7 +601,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
         if (owner) {                                           // the new token's score
 #pragma unroll
           for (int o = 8; o >= 1; o >>= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-          if (l16 == 0) sg.snew[r] = to_log2(z);
+          if (l16 == 0) sg.snew[r] = z * s_scale;
         }
         // The lane's channels 4 l16 .. are a quarter of chunk l16 / 4 (and of chunk
         // l16 / 4 + 4). bf16: the lanes of head r (4 r + tig) hold channels 2 tig,
@@ -625,7 +624,7 @@ decode_paged_kernel(const __grid_constant__ CUtensorMap tm_k,
       }
       if (lead && lane < 16) sg.sink[lane] = cur.sink;
       if (lead && lane == 0) {
-        sg.ks = to_log2(cur.ks);
+        sg.ks = s_scale;
         sg.vs = cur.vs;
         sg.dst = (unsigned)cur.page < (unsigned)a.c.num_pages
                      ? cur.page * a.c.page_stride + cur.slot * a.c.token_stride : -1;

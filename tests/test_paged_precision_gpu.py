@@ -94,3 +94,16 @@ def test_long_sums_are_not_cut_off(cuda_lib, dtype):
         e = torch.softmax(z, 0)[:-1]
         errors.append((out[0, h].double() - e @ V) / (e @ V.abs()))
     assert pp.rms(torch.stack(errors).cpu().numpy()) <= 2.0 ** -18
+
+
+@pytest.mark.parametrize("power", [-112, 112])
+def test_key_scales_near_the_ends_of_float32(cuda_lib, power):
+    """Neither the cached keys' scores nor the new one's pass through a product that is larger
+    or smaller than float32 holds."""
+    w = Paged([0, 0, 9, 65, 100] * 6, H=16, Hk=2, P=16, dtype=E4M3, seed=67)
+    w.k_scale = w.k_scale * 2.0 ** -power
+    w.wk = w.wk * 2.0 ** -power
+    w.wq = w.wq * 2.0 ** power
+    d = w.dev()
+    out, lse = decode(cuda_lib, w, d, 0, fp32_out=True)
+    pp.check(w, out, lse, d["kp"], d["vp"], 0)
